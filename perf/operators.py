@@ -262,7 +262,10 @@ def _blocks(t):
 def _plain_fp8(st):
     K, N = st["case"]["K"], st["case"]["N"]
     x = _blocks(st["x"].float())
-    scale = (x.abs().amax(dim=2) / E4M3_MAX).clamp_min(SCALE_MIN)
+    top = x.abs().amax(dim=2)
+    # a quotient of two tensors: by a plain number, torch multiplies by its
+    # rounded reciprocal instead
+    scale = (top / torch.full_like(top, E4M3_MAX)).clamp_min(SCALE_MIN)
     q = (x / scale[:, :, None]).to(torch.float8_e4m3fn)
     rows = (q.float() * scale[:, :, None]).view(x.shape[0], -1)[:, :K]
     ws = st["w_scale"][st["active"]].repeat_interleave(BLOCK, dim=1)[:, :N]
