@@ -271,6 +271,120 @@ coli_status coli_moe_combine_rows(int32_t T, int32_t k, int32_t H, const float *
 coli_status coli_moe_prefetch(const coli_moe *h, int32_t T, int32_t k, const int32_t *topk_idx,
                               size_t max_bytes, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- around the layer: norms, and experts that are not int4 -----------------
+ * These calls take no handle.  The pages describe the layer step only; a
+ * model's block around it, and experts kept in bf16 or 8-bit floating point,
+ * are library additions.  They follow the conventions above (device pointers,
+ * row-major and contiguous, 16-byte aligned; asynchronous on `stream`; host
+ * checks before any launch; T == 0 or R == 0 is a no-op unless stated). */
+
+/* Norms around a block with its gate, the residual scale and the residual sum,
+ * one pass over the rows (RMS norms, fp32 inside):
+ *   n[t] = y[t] / sqrt(mean(y[t]^2) + eps) * post_w   (post_w NULL: n = y)
+ *   s[t] = x[t] + alpha * g * n[t]                    (y NULL: s = x)
+ *   o[t] = s[t] / sqrt(mean(s[t]^2) + eps) * pre_w    (from the unrounded s)
+ *   x      [T][H] in   the residual stream (x_dtype)
+ *   y      [T][H] in   the block's output (y_dtype), e.g. coli_moe_layer's
+ *                      `out`; nullable
+ *   post_w [H] fp32 nullable: the norm after the block
+ *   gate   fp32: [H] (COLI_GATE_CHANNEL), [T] (COLI_GATE_TOKEN), or NULL
+ *          (COLI_GATE_NONE: g = 1)
+ *   pre_w  [H] fp32: the norm before the next block; needed with `o`
+ *   s_out  [T][H] out, x_dtype, nullable; may be x itself
+ *   o      [T][H] out, o_dtype, nullable; may be y itself when the types agree
+ * Errors: INVALID_ARG (negative sizes or eps, bad enum, neither s_out nor o, o
+ * without pre_w, post_w or gate without y, a gate that does not match
+ * gate_kind), SHAPE (H > 16384, T > 2^24), ALIGN. */
+#define COLI_GATE_NONE 0
+#define COLI_GATE_CHANNEL 1
+#define COLI_GATE_TOKEN 2
+coli_status coli_moe_block_norm(int32_t T, int32_t H, const void *x, coli_out_dtype x_dtype,
+                                const void *y, coli_out_dtype y_dtype, const float *post_w,
+                                const float *gate, int32_t gate_kind, float alpha,
+                                const float *pre_w, float eps, void *s_out, void *o,
+                                coli_out_dtype o_dtype, void *stream);
+
+/* Gradients of coli_moe_block_norm, from the stored s and y:
+ *   d_o    [T][H] o_dtype, nullable: gradient of o (with it: s and pre_w)
+ *   d_s    [T][H] x_dtype, nullable: gradient of s from elsewhere (the
+ *          residual stream); at least one of d_o and d_s
+ *   s      [T][H] x_dtype: what the forward call stored in s_out
+ *   y, post_w, gate, gate_kind, alpha, pre_w, eps: as the forward call
+ *   dx     [T][H] x_dtype, dy [T][H] y_dtype: nullable outputs; dx may be d_s
+ *          itself, dy may be y itself or, when the types agree, d_o itself
+ *   dpre_w [H], dpost_w [H], dgate ([H] or [T], as gate) fp32: nullable
+ *          outputs, overwritten; sums in a fixed order (the same bits every
+ *          call); zeros when T == 0 (dgate: [H])
+ *   ws     needed for dpre_w, dpost_w and a channel gate's dgate: at least
+ *          coli_moe_block_norm_workspace_size(T, H) bytes, 256-byte aligned
+ *          (needs no clear)
+ * Errors: as the forward call; INVALID_ARG also for a gradient of something
+ * the call does not have; WORKSPACE. */
+size_t coli_moe_block_norm_workspace_size(int32_t T, int32_t H);
+coli_status coli_moe_block_norm_backward(
+    int32_t T, int32_t H, const void *d_o, coli_out_dtype o_dtype, const void *d_s, const void *s,
+    coli_out_dtype x_dtype, const void *y, coli_out_dtype y_dtype, const float *post_w,
+    const float *gate, int32_t gate_kind, float alpha, const float *pre_w, float eps, void *dx,
+    void *dy, float *dpre_w, float *dpost_w, float *dgate, void *ws, size_t ws_bytes,
+    void *stream);
+
+/* Matrix products of rows grouped by expert, ragged group sizes.  Rows
+ * offsets[e] .. offsets[e+1] - 1 belong to expert e (`offsets` as
+ * coli_moe_union writes it: [E+1] int32, ascending, within [0, R]):
+ *   coli_moe_grouped_mm     out[r][n]   = sum_k x[r][k] w[e][n][k]
+ *   coli_moe_grouped_mm_dx  dx[r][k]    = sum_n dy[r][n] w[e][n][k]
+ *   coli_moe_grouped_mm_dw  dw[e][n][k] (+)= sum_{r of e} dy[r][n] x[r][k]
+ *   x [R][K], dy [R][N], w [E][N][K] bf16; out [R][N], dx [R][K], dw [E][N][K]
+ *   fp32 or bf16, fp32 sums rounded once.  N and K multiples of 8, at most
+ *   65536.  E = 1 is a dense layer.
+ * Rows of no group (before offsets[0], from offsets[E] on) are left as they
+ * were.  dw of an expert without rows is zero; with `accumulate` (non-zero)
+ * the products are added to what dw holds, and R == 0 leaves it as it was.
+ * The same call gives the same bits every time.  The output must not overlap
+ * an input.
+ *   ws  at least coli_moe_grouped_workspace_size(R, E) bytes, 256-byte
+ *       aligned, cleared once (coli_moe_workspace_clear); it may be a layer's
+ *       workspace of that size.  Device-side errors in its status word:
+ *       BAD_INDEX (offsets that descend or leave [0, R]: those groups are
+ *       skipped), TIMEOUT.
+ * Errors: INVALID_ARG (NULL, negative sizes, bad enum), SHAPE (E > 1024,
+ * R > 2^24, N or K), ALIGN, WORKSPACE. */
+size_t coli_moe_grouped_workspace_size(int32_t R, int32_t E);
+coli_status coli_moe_grouped_mm(int32_t R, int32_t E, int32_t N, int32_t K, const void *x_bf16,
+                                const void *w_bf16, const int32_t *offsets, void *out,
+                                coli_out_dtype out_dtype, void *ws, size_t ws_bytes, void *stream);
+coli_status coli_moe_grouped_mm_dx(int32_t R, int32_t E, int32_t N, int32_t K,
+                                   const void *dy_bf16, const void *w_bf16, const int32_t *offsets,
+                                   void *dx, coli_out_dtype dx_dtype, void *ws, size_t ws_bytes,
+                                   void *stream);
+coli_status coli_moe_grouped_mm_dw(int32_t R, int32_t E, int32_t N, int32_t K,
+                                   const void *dy_bf16, const void *x_bf16, const int32_t *offsets,
+                                   void *dw, coli_out_dtype dw_dtype, int32_t accumulate, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/* Rows to 8-bit floating point (e4m3), one fp32 scale per row and 128 values:
+ *   scales[b][r] = max(max_{k of block b} |x[r][k]| / 448, 2^-126)
+ *   q[r][k]      = e4m3(x[r][k] / scales[b][r]), the quotient rounded to fp32,
+ *                  then to nearest even
+ *   x [R][K] bf16 or fp32, q [R][K], scales [ceil(K/128)][R] (block-major);
+ *   K a multiple of 16, at most 65536 (the last block may be short).
+ * A block that holds a NaN or an infinity gets a NaN or infinite scale, and
+ * its row's products are NaN.  Errors: INVALID_ARG, SHAPE, ALIGN. */
+coli_status coli_moe_fp8_quantize_rows(int32_t R, int32_t K, const void *x, coli_out_dtype x_dtype,
+                                       uint8_t *q, float *scales, void *stream);
+
+/* The grouped product in 8-bit floating point with a scale for each block of
+ * 128 (rows: 1 x 128, weights: 128 x 128), fp32 sums:
+ *   out[r][n] = sum_b x_scale[b][r] w_scale[e][n/128][b]
+ *                     sum_{k of block b} xq[r][k] wq[e][n][k]
+ *   xq, x_scale as coli_moe_fp8_quantize_rows writes them; wq [E][N][K] e4m3,
+ *   w_scale [E][ceil(N/128)][ceil(K/128)] fp32; K a multiple of 16, N of 8.
+ *   Everything else as coli_moe_grouped_mm. */
+coli_status coli_moe_fp8_grouped_mm(int32_t R, int32_t E, int32_t N, int32_t K, const uint8_t *xq,
+                                    const float *x_scale, const uint8_t *wq, const float *w_scale,
+                                    const int32_t *offsets, void *out, coli_out_dtype out_dtype,
+                                    void *ws, size_t ws_bytes, void *stream);
+
 /* Synchronise `stream` and return the workspace's device status word
  * (COLI_OK, COLI_ERR_BAD_INDEX or COLI_ERR_TIMEOUT), or COLI_ERR_CUDA if the
  * stream reports an error.  The word stays set until coli_moe_workspace_clear. */

@@ -33,12 +33,20 @@ COLI_WS_LOGITS_OFFSET = 16384  # router logits left in the workspace by coli_moe
 COLI_WS_HEADER_BYTES = 16384
 COLI_OUT_BF16 = 1
 COLI_GROUP_PER_ROW = 0  # coli_moe_desc.group_size of the per-row int4 format
+COLI_GATE_NONE = 0      # gate_kind of coli_moe_block_norm: no gate,
+COLI_GATE_CHANNEL = 1   # one value per channel [H],
+COLI_GATE_TOKEN = 2     # one value per token [T]
 
 EXPORTS = ("coli_moe_create", "coli_moe_destroy", "coli_moe_workspace_size",
            "coli_moe_workspace_clear", "coli_moe_route", "coli_moe_union",
            "coli_moe_union_workspace_size", "coli_moe_ffn",
            "coli_moe_layer", "coli_moe_layer_noalloc", "coli_moe_combine_rows",
            "coli_moe_prefetch",
+           "coli_moe_block_norm", "coli_moe_block_norm_backward",
+           "coli_moe_block_norm_workspace_size",
+           "coli_moe_grouped_mm", "coli_moe_grouped_mm_dx", "coli_moe_grouped_mm_dw",
+           "coli_moe_grouped_workspace_size",
+           "coli_moe_fp8_quantize_rows", "coli_moe_fp8_grouped_mm",
            "coli_moe_get_status",
            "coli_moe_debug_inject",
            "coli_moe_profile_enable",
@@ -94,6 +102,26 @@ def _load():
     L.coli_moe_combine_rows.restype = ctypes.c_int
     L.coli_moe_prefetch.argtypes = [P, i32, i32, P, sz, P, sz, P]
     L.coli_moe_prefetch.restype = ctypes.c_int
+    f32, ci = ctypes.c_float, ctypes.c_int
+    L.coli_moe_block_norm.argtypes = [i32, i32, P, ci, P, ci, P, P, i32, f32, P, f32, P, P, ci, P]
+    L.coli_moe_block_norm.restype = ctypes.c_int
+    L.coli_moe_block_norm_workspace_size.argtypes = [i32, i32]
+    L.coli_moe_block_norm_workspace_size.restype = sz
+    L.coli_moe_block_norm_backward.argtypes = [i32, i32, P, ci, P, P, ci, P, ci, P, P, i32, f32, P,
+                                               f32, P, P, P, P, P, P, sz, P]
+    L.coli_moe_block_norm_backward.restype = ctypes.c_int
+    L.coli_moe_grouped_workspace_size.argtypes = [i32, i32]
+    L.coli_moe_grouped_workspace_size.restype = sz
+    L.coli_moe_grouped_mm.argtypes = [i32, i32, i32, i32, P, P, P, P, ci, P, sz, P]
+    L.coli_moe_grouped_mm.restype = ctypes.c_int
+    L.coli_moe_grouped_mm_dx.argtypes = [i32, i32, i32, i32, P, P, P, P, ci, P, sz, P]
+    L.coli_moe_grouped_mm_dx.restype = ctypes.c_int
+    L.coli_moe_grouped_mm_dw.argtypes = [i32, i32, i32, i32, P, P, P, P, ci, i32, P, sz, P]
+    L.coli_moe_grouped_mm_dw.restype = ctypes.c_int
+    L.coli_moe_fp8_quantize_rows.argtypes = [i32, i32, P, ci, P, P, P]
+    L.coli_moe_fp8_quantize_rows.restype = ctypes.c_int
+    L.coli_moe_fp8_grouped_mm.argtypes = [i32, i32, i32, i32, P, P, P, P, P, P, ci, P, sz, P]
+    L.coli_moe_fp8_grouped_mm.restype = ctypes.c_int
     L.coli_moe_get_status.argtypes = [P, P]
     L.coli_moe_get_status.restype = ctypes.c_int
     L.coli_moe_debug_inject.argtypes = [i32]
@@ -228,6 +256,180 @@ def coli_moe_profile_read():
     s = lib.coli_moe_profile_read(ms, ctypes.byref(n))
     _check(s, "coli_moe_profile_read", True)
     return list(ms), int(n.value)
+
+
+# ---- around the layer: norms and grouped products ---------------------------
+# These functions know every argument's size, so they also check the tensors'
+# types, element counts and device before any pointer is passed, and run on
+# the device of their tensors (its current stream by default).
+
+_DTYPE = {torch.float32: COLI_OUT_F32, torch.bfloat16: COLI_OUT_BF16}
+
+
+def _arg(t, name, numel, dtypes, device, optional=False):
+    """Pointer of a checked tensor argument (None for an absent optional one)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must live on the CUDA device")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: type {t.dtype} is not one of {tuple(dtypes)}")
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, the call's sizes need {numel}")
+    return t.data_ptr()
+
+
+_F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _device(*tensors):
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            return t.device
+    raise ValueError("no tensor argument")
+
+
+def _run(fn, device, stream, *args):
+    """fn(*args, stream) on `device`."""
+    if device.type != "cuda":
+        raise ValueError("tensor arguments must live on the CUDA device")
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def _ws_arg(ws, device):
+    """(pointer, bytes) of a workspace tensor of any type; (None, 0) for None."""
+    if ws is None:
+        return None, 0
+    n = ws.numel()
+    return _arg(ws, "ws", n, (ws.dtype,), device), n * ws.element_size()
+
+
+def coli_moe_block_norm(T, H, x, y, post_w, gate, gate_kind, alpha, pre_w, eps, s_out, o,
+                        stream=None, raise_on_error=True):
+    """s = x + alpha * g * norm(y) post_w;  o = norm(s) pre_w (include/coli_moe.h).
+    x and s_out share one type, y and o have their own (fp32 or bf16)."""
+    dev = _device(x, s_out, o)
+    n = T * H
+    args = (T, H, _arg(x, "x", n, _DTYPE, dev), _DTYPE[x.dtype],
+            _arg(y, "y", n, _DTYPE, dev, True), _DTYPE[y.dtype] if y is not None else 0,
+            _arg(post_w, "post_w", H, _F32, dev, True),
+            _arg(gate, "gate", T if gate_kind == COLI_GATE_TOKEN else H, _F32, dev, True),
+            gate_kind, alpha, _arg(pre_w, "pre_w", H, _F32, dev, True), eps,
+            _arg(s_out, "s_out", n, (x.dtype,), dev, True), _arg(o, "o", n, _DTYPE, dev, True),
+            _DTYPE[o.dtype] if o is not None else 0)
+    s = _run(lib.coli_moe_block_norm, dev, stream, *args)
+    return _check(s, "coli_moe_block_norm", raise_on_error)
+
+
+def coli_moe_block_norm_workspace_size(T, H):
+    return int(lib.coli_moe_block_norm_workspace_size(T, H))
+
+
+def coli_moe_block_norm_backward(T, H, d_o, d_s, s, y, post_w, gate, gate_kind, alpha, pre_w, eps,
+                                 dx, dy, dpre_w, dpost_w, dgate, ws=None, stream=None,
+                                 raise_on_error=True):
+    """Gradients of coli_moe_block_norm from the stored s and y
+    (include/coli_moe.h)."""
+    dev = _device(d_o, d_s, s, y, dx, dy, dpre_w, dpost_w, dgate)
+    n = T * H
+    stream_t = next((t for t in (s, d_s, dx) if t is not None), None)
+    xt = stream_t.dtype if stream_t is not None else torch.float32
+    if xt not in _DTYPE:
+        raise ValueError(f"type {xt} is not one of {tuple(_DTYPE)}")
+    yt = y.dtype if y is not None else torch.float32
+    n_gate = T if gate_kind == COLI_GATE_TOKEN else H
+    ws_p, ws_n = _ws_arg(ws, dev)
+    args = (T, H, _arg(d_o, "d_o", n, _DTYPE, dev, True),
+            _DTYPE[d_o.dtype] if d_o is not None else 0,
+            _arg(d_s, "d_s", n, (xt,), dev, True), _arg(s, "s", n, (xt,), dev, True), _DTYPE[xt],
+            _arg(y, "y", n, _DTYPE, dev, True), _DTYPE[yt] if y is not None else 0,
+            _arg(post_w, "post_w", H, _F32, dev, True), _arg(gate, "gate", n_gate, _F32, dev, True),
+            gate_kind, alpha, _arg(pre_w, "pre_w", H, _F32, dev, True), eps,
+            _arg(dx, "dx", n, (xt,), dev, True), _arg(dy, "dy", n, (yt,), dev, True),
+            _arg(dpre_w, "dpre_w", H, _F32, dev, True),
+            _arg(dpost_w, "dpost_w", H, _F32, dev, True),
+            _arg(dgate, "dgate", n_gate, _F32, dev, True), ws_p, ws_n)
+    st = _run(lib.coli_moe_block_norm_backward, dev, stream, *args)
+    return _check(st, "coli_moe_block_norm_backward", raise_on_error)
+
+
+def coli_moe_grouped_workspace_size(R, E):
+    return int(lib.coli_moe_grouped_workspace_size(R, E))
+
+
+def grouped_workspace(R, E, device="cuda"):
+    """A cleared workspace for the grouped products of up to R rows."""
+    ws = torch.empty(coli_moe_grouped_workspace_size(R, E), dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        coli_moe_workspace_clear(ws)
+    return ws
+
+
+def coli_moe_grouped_mm(R, E, N, K, x, w, offsets, out, ws, stream=None, raise_on_error=True):
+    """out[r] = w[e] x[r] for the rows of each expert (include/coli_moe.h)."""
+    dev = _device(x, w, out)
+    s = _run(lib.coli_moe_grouped_mm, dev, stream, R, E, N, K, _arg(x, "x", R * K, _BF16, dev),
+             _arg(w, "w", E * N * K, _BF16, dev), _arg(offsets, "offsets", E + 1, _I32, dev),
+             _arg(out, "out", R * N, _DTYPE, dev), _DTYPE[out.dtype], *_ws_arg(ws, dev))
+    return _check(s, "coli_moe_grouped_mm", raise_on_error)
+
+
+def coli_moe_grouped_mm_dx(R, E, N, K, dy, w, offsets, dx, ws, stream=None, raise_on_error=True):
+    """dx[r] = w[e]^T dy[r] (include/coli_moe.h)."""
+    dev = _device(dy, w, dx)
+    s = _run(lib.coli_moe_grouped_mm_dx, dev, stream, R, E, N, K,
+             _arg(dy, "dy", R * N, _BF16, dev), _arg(w, "w", E * N * K, _BF16, dev),
+             _arg(offsets, "offsets", E + 1, _I32, dev), _arg(dx, "dx", R * K, _DTYPE, dev),
+             _DTYPE[dx.dtype], *_ws_arg(ws, dev))
+    return _check(s, "coli_moe_grouped_mm_dx", raise_on_error)
+
+
+def coli_moe_grouped_mm_dw(R, E, N, K, dy, x, offsets, dw, accumulate, ws, stream=None,
+                           raise_on_error=True):
+    """dw[e] (+)= sum over the rows of e of dy[r] x[r]^T (include/coli_moe.h)."""
+    dev = _device(dy, x, dw)
+    s = _run(lib.coli_moe_grouped_mm_dw, dev, stream, R, E, N, K,
+             _arg(dy, "dy", R * N, _BF16, dev), _arg(x, "x", R * K, _BF16, dev),
+             _arg(offsets, "offsets", E + 1, _I32, dev), _arg(dw, "dw", E * N * K, _DTYPE, dev),
+             _DTYPE[dw.dtype], 1 if accumulate else 0, *_ws_arg(ws, dev))
+    return _check(s, "coli_moe_grouped_mm_dw", raise_on_error)
+
+
+def coli_moe_fp8_quantize_rows(R, K, x, q, scales, stream=None, raise_on_error=True):
+    """Rows to e4m3 with one fp32 scale per row and 128 values; scales is
+    [ceil(K/128)][R] (include/coli_moe.h)."""
+    dev = _device(x, q, scales)
+    s = _run(lib.coli_moe_fp8_quantize_rows, dev, stream, R, K, _arg(x, "x", R * K, _DTYPE, dev),
+             _DTYPE[x.dtype], _arg(q, "q", R * K, _E4M3, dev),
+             _arg(scales, "scales", -(-K // 128) * R, _F32, dev))
+    return _check(s, "coli_moe_fp8_quantize_rows", raise_on_error)
+
+
+def coli_moe_fp8_grouped_mm(R, E, N, K, xq, x_scale, wq, w_scale, offsets, out, ws, stream=None,
+                            raise_on_error=True):
+    """The grouped product of e4m3 rows and weights with their block scales
+    (include/coli_moe.h)."""
+    dev = _device(xq, wq, out)
+    kb = -(-K // 128)
+    s = _run(lib.coli_moe_fp8_grouped_mm, dev, stream, R, E, N, K,
+             _arg(xq, "xq", R * K, _E4M3, dev), _arg(x_scale, "x_scale", kb * R, _F32, dev),
+             _arg(wq, "wq", E * N * K, _E4M3, dev),
+             _arg(w_scale, "w_scale", E * -(-N // 128) * kb, _F32, dev),
+             _arg(offsets, "offsets", E + 1, _I32, dev), _arg(out, "out", R * N, _DTYPE, dev),
+             _DTYPE[out.dtype], *_ws_arg(ws, dev))
+    return _check(s, "coli_moe_fp8_grouped_mm", raise_on_error)
 
 
 # ---- handle ---------------------------------------------------------------
