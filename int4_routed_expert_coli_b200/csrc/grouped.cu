@@ -56,10 +56,11 @@ constexpr int kMaxStages = 12;
 constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kMaxGrid = 148;
-constexpr int kChunk = 32;             // bf16 K-blocks per accumulator chain
+constexpr int kChunk = 8;              // bf16 K-blocks per accumulator chain
 constexpr int kScaleBufs = 4;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kMinRange = 4;           // K-blocks of a range of the last wave, at least
+constexpr int kStoreBytes = 32 * 128;  // kDw: staging of one warp's stores
 
 struct MmArgs {
     const int* offsets;   // [E + 1]
@@ -76,17 +77,24 @@ struct MmArgs {
     int* status;
 };
 
-template <int MODE, bool FP8, int BN_>
+// CTAS = 2: a pair of CTAs works on one tile of 256 M rows.  Each holds its
+// 128 rows of A and half of the columns of B; the even one issues the MMAs of
+// both (cta_group::2), each drains its own 128 rows.
+template <int MODE, bool FP8, int BN_, int CTAS_>
 struct Cfg {
-    static constexpr int BN = BN_;
+    static constexpr int BN = BN_, CTAS = CTAS_;
     static constexpr int BK = FP8 ? 128 : 64;              // reduction per stage
-    static constexpr int kBoxRows = BN >= 256 ? 64 : 16;   // rows per B tensor copy
-    static constexpr int kBBytes = BN * kRowBytes;
+    static constexpr int kBoxRows = BN == 256 ? 32 : 16;   // rows per B tensor copy, and
+    static constexpr int kBigBox = BN == 256 ? 128 : 64;   // rows of the copies of whole parts
+    static constexpr int kBBytes = BN / CTAS * kRowBytes;
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kTmemCols = 2 * BN;
+    static constexpr int kNGrain = 16 * CTAS;              // MMA N in multiples of this
     static constexpr bool kAMn = MODE != kFwd;
     static constexpr bool kBMn = MODE == kDw;
     static constexpr int kAcc = BN / 2;                    // accumulators per epilogue thread
+    static constexpr int kScaleBytes = FP8 ? kScaleBufs * BN * 4 : 0;
+    static constexpr int kStoreStage = MODE == kDw ? kEpiWarps * kStoreBytes : 0;
 };
 
 // Everything of shared memory but the stages.
@@ -94,87 +102,99 @@ struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t sc_full[kScaleBufs], sc_empty[kScaleBufs];
+    uint64_t tail_ready[kMaxStages];       // kDw, CTAS = 2: the odd CTA's rows are cleared
     uint32_t tmem;
     int abort;
     int last;                              // this CTA finishes the cut tile
+    int whole, wave, range;                // whole tiles; steps of the last wave, of a range of it
+    long long base;                        // first step of the last wave
     long long scan[2][kThreads / 32 + 1];
     int tile0[kMaxExperts + 1];            // first tile (of the first M tile column) of each group
     long long step0[kMaxExperts + 1];      // K-block steps before each group
 };
 constexpr int kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
-template <class C, bool FP8>
-constexpr int scale_bytes() { return FP8 ? kScaleBufs * C::BN * 4 : 0; }
-template <class C, bool FP8>
+template <class C>
+constexpr int fixed_smem() { return 1024 + kSharedBytes + C::kScaleBytes + C::kStoreStage; }
+template <class C>
 constexpr int stage_count() {
-    return std::min(kMaxStages, (kSmemMax - 1024 - kSharedBytes - scale_bytes<C, FP8>()) / C::kStage);
+    return std::min(kMaxStages, (kSmemMax - fixed_smem<C>()) / C::kStage);
 }
 
 // A piece of work: K-blocks [kb0, kb1) of one tile.
 struct Piece {
-    int e, m0;
+    int e, m0;           // expert; first M row of this CTA
     int row0, rows;      // kFwd, kDx: the tile's rows; kDw: the group's
     int col0;            // kDw: first column
     int n;               // valid columns of the MMA N dimension
     int kb0, kb1, kb;    // of kb
-    long long step;      // of the tile's first K-block, relative to the last wave
+    int step;            // of the tile's first K-block in the last wave's sequence
 };
 
-// Where this CTA is in its sequence of pieces; every role walks its own copy.
+// The sequence of pieces of one CTA (of a pair, CTAS = 2: both CTAs walk the
+// same tiles, each with its own M rows); every role walks its own copy.  Tiles
+// and the steps of one wave fit 32 bits for every size the host lets through
+// (R at most 2^24, M and the columns at most 2^16); step0 counts in 64.
 template <int MODE, class C>
 struct Walk {
     const MmArgs& a;
     const Shared& s;
-    int m_tiles, c_tiles;
-    long long full;              // tiles dealt whole
-    long long tile;              // next of those
-    long long cur, end, base;    // next step and end of this CTA's range; first step of the wave
+    int tile;        // next of the tiles dealt whole
+    int cur, end;    // next step and end of this worker's range of the last wave
 
-    __device__ __forceinline__ Walk(const MmArgs& a_, const Shared& s_) : a(a_), s(s_) {
-        m_tiles = (a.M + kBM - 1) / kBM;
-        c_tiles = MODE == kDw ? (a.cols + C::BN - 1) / C::BN : 1;
-        const long long per = (long long)m_tiles * c_tiles;
-        const long long tiles = s.tile0[a.E] * per;
-        full = tiles - tiles % gridDim.x;
-        tile = blockIdx.x;
-        const long long steps = s.step0[a.E] * per;
-        base = full < tiles ? step_of(full) : steps;
-        const long long q = range();
-        cur = base + min(steps - base, q * blockIdx.x);
-        end = base + min(steps - base, q * (blockIdx.x + 1));
+    static __device__ __forceinline__ int worker() { return blockIdx.x / C::CTAS; }
+    static __device__ __forceinline__ int workers() { return gridDim.x / C::CTAS; }
+    static __device__ __forceinline__ int rank() { return blockIdx.x % C::CTAS; }
+    static __device__ __forceinline__ int m_tiles(const MmArgs& a) {
+        return (a.M + kBM * C::CTAS - 1) / (kBM * C::CTAS);
     }
-    // K-blocks of one CTA's range of the last wave
-    __device__ __forceinline__ long long range() const {
-        const long long n = s.step0[a.E] * ((long long)m_tiles * c_tiles) - base;
-        return max((long long)kMinRange, (n + gridDim.x - 1) / gridDim.x);
+    static __device__ __forceinline__ int c_tiles(const MmArgs& a) {
+        return MODE == kDw ? (a.cols + C::BN - 1) / C::BN : 1;
     }
-    __device__ __forceinline__ int group_kb(int e) const {
+    static __device__ __forceinline__ int group_kb(const MmArgs& a, int e) {
         if (MODE != kDw) return (a.red + C::BK - 1) / C::BK;
         const int rows = __ldg(a.offsets + e + 1) - __ldg(a.offsets + e);
         return max(1, (rows + C::BK - 1) / C::BK);
     }
-    __device__ __forceinline__ int group_of_tile(long long t) const {
-        const long long per = (long long)m_tiles * c_tiles;
-        int lo = 0, hi = a.E;
+    // The last group with first[e] * per <= v.
+    template <typename T>
+    static __device__ __forceinline__ int group_of(const T* first, long long per, long long v, int E) {
+        int lo = 0, hi = E;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (s.tile0[mid] * per <= t) lo = mid;
+            if (first[mid] * per <= v) lo = mid;
             else hi = mid;
         }
         return lo;
     }
-    __device__ __forceinline__ long long step_of(long long t) const {
-        const long long per = (long long)m_tiles * c_tiles;
-        const int e = group_of_tile(t);
-        return s.step0[e] * per + (t - s.tile0[e] * per) * group_kb(e);
+    // Where the whole tiles end and how the last wave is cut (one thread).
+    static __device__ __forceinline__ void plan(const MmArgs& a, Shared& s) {
+        const long long per = (long long)m_tiles(a) * c_tiles(a);
+        const long long tiles = s.tile0[a.E] * per, steps = s.step0[a.E] * per;
+        const long long full = tiles - tiles % workers();
+        long long base = steps;
+        if (full < tiles) {
+            const int e = group_of(s.tile0, per, full, a.E);
+            base = s.step0[e] * per + (full - s.tile0[e] * per) * group_kb(a, e);
+        }
+        s.whole = (int)full;
+        s.base = base;
+        s.wave = (int)(steps - base);
+        s.range = max(kMinRange, (s.wave + workers() - 1) / workers());
     }
-    __device__ __forceinline__ void fill(Piece& p, int e, long long t, int kb) const {
+    __device__ __forceinline__ Walk(const MmArgs& a_, const Shared& s_) : a(a_), s(s_) {
+        tile = worker();
+        cur = (int)min((long long)s.wave, (long long)s.range * worker());
+        end = min(s.wave, cur + s.range);
+    }
+    __device__ __forceinline__ void fill(Piece& p, int e, int t, int kb) const {
         const int off = __ldg(a.offsets + e), rows = __ldg(a.offsets + e + 1) - off;
         p.e = e;
         p.kb = kb;
         if (MODE == kDw) {
-            p.m0 = (int)(t / c_tiles) * kBM;
-            p.col0 = (int)(t % c_tiles) * C::BN;
+            const int ct = c_tiles(a);
+            p.m0 = (t / ct * C::CTAS + rank()) * kBM;
+            p.col0 = t % ct * C::BN;
             p.n = min(C::BN, a.cols - p.col0);
             p.row0 = off;
             p.rows = rows;
@@ -182,68 +202,114 @@ struct Walk {
             // a group's rows are shared evenly by its row tiles (16-row grain)
             const int nt = s.tile0[e + 1] - s.tile0[e];
             const int bn = ((rows + nt - 1) / nt + 15) & ~15;
-            const int i = (int)(t % nt) * bn;
-            p.m0 = (int)(t / nt) * kBM;
+            const int i = t % nt * bn;
+            p.m0 = (t / nt * C::CTAS + rank()) * kBM;
             p.col0 = 0;
             p.row0 = off + i;
             p.rows = p.n = max(0, min(bn, rows - i));
         }
     }
     __device__ __forceinline__ bool next(Piece& p) {
-        const long long per = (long long)m_tiles * c_tiles;
-        if (tile < full) {
-            const int e = group_of_tile(tile), kb = group_kb(e);
-            fill(p, e, tile - s.tile0[e] * per, kb);
+        const long long per = (long long)m_tiles(a) * c_tiles(a);
+        if (tile < s.whole) {
+            const int e = group_of(s.tile0, per, tile, a.E), kb = group_kb(a, e);
+            fill(p, e, (int)(tile - s.tile0[e] * per), kb);
             p.kb0 = 0;
             p.kb1 = kb;
-            p.step = -1;
-            tile += gridDim.x;
+            p.step = 0;
+            tile += workers();
             return true;
         }
         if (cur >= end) return false;
-        int lo = 0, hi = a.E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s.step0[mid] * per <= cur) lo = mid;
-            else hi = mid;
-        }
-        const int kb = group_kb(lo);
-        const long long in = cur - s.step0[lo] * per, t = in / kb;
-        fill(p, lo, t, kb);
-        p.kb0 = (int)(in - t * kb);
-        p.kb1 = (int)min((long long)kb, p.kb0 + (end - cur));
-        p.step = cur - p.kb0 - base;
+        const long long at = s.base + cur;
+        const int e = group_of(s.step0, per, at, a.E), kb = group_kb(a, e);
+        const long long in = at - s.step0[e] * per;
+        const int t = (int)(in / kb);
+        fill(p, e, t, kb);
+        p.kb0 = (int)(in - (long long)t * kb);
+        p.kb1 = min(kb, p.kb0 + (end - cur));
+        p.step = cur - p.kb0;
         cur += p.kb1 - p.kb0;
         return true;
     }
 };
 
-// Columns of the MMA: the valid ones rounded up to 16.
-__device__ __forceinline__ int mma_n(int n) { return max(16, (n + 15) & ~15); }
+// Columns of the MMA: the valid ones rounded up to its grain.
+template <class C>
+__device__ __forceinline__ int mma_n(int n) {
+    return (max(n, 1) + C::kNGrain - 1) / C::kNGrain * C::kNGrain;
+}
 
-template <int MODE, bool FP8, int BN_>
+// Add one accumulator's columns (times their scales) to a thread's sums.  The
+// loads of 16 columns run under the sums of the 16 before; a whole tile's loop
+// has no branches, so its instructions interleave.
+template <class C, bool FP8, bool WHOLE>
+__device__ __forceinline__ void drain(uint32_t src, const float* sc, int nc, float (&acc)[C::kAcc]) {
+    constexpr int kGroups = C::kAcc / 16;
+    uint32_t v[2][16];
+    tc::ld16(src, v[0]);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        if (!WHOLE && g * 16 >= nc) break;
+        float4 f[4];
+        if constexpr (FP8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = reinterpret_cast<const float4*>(sc + g * 16)[j];
+        }
+        uint32_t(&w)[16] = v[g & 1];
+        tc::ld_wait(w);
+        if (g + 1 < kGroups && (WHOLE || (g + 1) * 16 < nc))
+            tc::ld16(src + (g + 1) * 16, v[(g + 1) & 1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float* d = acc + g * 16 + 4 * j;
+            if constexpr (FP8) {
+                d[0] += __uint_as_float(w[4 * j]) * f[j].x;
+                d[1] += __uint_as_float(w[4 * j + 1]) * f[j].y;
+                d[2] += __uint_as_float(w[4 * j + 2]) * f[j].z;
+                d[3] += __uint_as_float(w[4 * j + 3]) * f[j].w;
+            } else {
+                d[0] += __uint_as_float(w[4 * j]);
+                d[1] += __uint_as_float(w[4 * j + 1]);
+                d[2] += __uint_as_float(w[4 * j + 2]);
+                d[3] += __uint_as_float(w[4 * j + 3]);
+            }
+        }
+    }
+}
+
+template <int MODE, bool FP8, int BN_, int CTAS_>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
-                  const __grid_constant__ CUtensorMap bmap, const MmArgs a) {
-    using C = Cfg<MODE, FP8, BN_>;
-    constexpr int kStages = stage_count<C, FP8>();
+                  const __grid_constant__ CUtensorMap bmap,
+                  const __grid_constant__ CUtensorMap bmap_big,
+                  const __grid_constant__ CUtensorMap omap, const MmArgs a) {
+    using C = Cfg<MODE, FP8, BN_, CTAS_>;
+    constexpr int kStages = stage_count<C>();
+    constexpr int CTAS = C::CTAS;
+    // Wide tiles hold 128 accumulators and 32 loaded values per epilogue
+    // thread: the epilogue's two warpgroups take registers from the first
+    // (128 x 72 + 256 x 216 = 384 x 168).
+    constexpr bool kSplitRegs = C::kAcc > 64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage0 = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* scale0 = reinterpret_cast<float*>(stage0 + (size_t)kStages * C::kStage);
-    Shared& s = *reinterpret_cast<Shared*>(stage0 + (size_t)kStages * C::kStage +
-                                           scale_bytes<C, FP8>());
+    uint8_t* store0 = stage0 + (size_t)kStages * C::kStage;
+    float* scale0 = reinterpret_cast<float*>(store0 + C::kStoreStage);
+    Shared& s = *reinterpret_cast<Shared*>(store0 + C::kStoreStage + C::kScaleBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CTAS == 2 ? tc::cta_rank() : 0;
     volatile int* abort = &s.abort;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
+            mbar_init(&s.tail_ready[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.acc_full[i], 1);
-            mbar_init(&s.acc_empty[i], kEpiWarps);
+            mbar_init(&s.acc_empty[i], kEpiWarps * CTAS);
         }
         for (int i = 0; i < kScaleBufs; ++i) {
             mbar_init(&s.sc_full[i], 1);
@@ -252,13 +318,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
         s.abort = 0;
         fence_barrier_init();
     }
-    if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr(&s.tmem)),
-                     "r"(C::kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == 2) tc::alloc<CTAS>(&s.tmem, C::kTmemCols);
     pdl_launch_dependents();
     pdl_wait();
 
@@ -317,8 +377,11 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
             bw += w[i];
         }
     }
+    __syncthreads();
+    if (threadIdx.x == 0) Walk<MODE, C>::plan(a, s);
     tc::fence_before();
     __syncthreads();
+    if constexpr (CTAS == 2) tc::cluster_sync();  // the pair's barriers are ready
     tc::fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
 
@@ -328,127 +391,204 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
         *abort = 1;
     };
     Walk<MODE, C> walk(a, s);
-    Piece p;
+    Piece p = {};
 
-    if (warp == 0) {
-        // ------------------------------- loads ---------------------------------
-        if (lane == 0) {
-            uint32_t it = 0;
-            while (!*abort && walk.next(p)) {
-                if (MODE == kDw && p.rows == 0) continue;  // nothing to add up
-                const int boxes = MODE == kDw ? (p.n + 63) / 64
-                                              : (p.n + C::kBoxRows - 1) / C::kBoxRows;
-                const uint32_t bytes =
-                    kABytes + boxes * (MODE == kDw ? 64 : C::kBoxRows) * kRowBytes;
-                bool ok = true;
-                for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                    const int i = it % kStages;
-                    if (it >= kStages && !mbar_wait(&s.empty[i], (it / kStages - 1) & 1)) {
+    if (warp < kEpiWarp0) {
+        if constexpr (kSplitRegs) tc::regs_dec<72>();
+        if (warp == 0) {
+            // ------------------------------ loads --------------------------------
+            if (lane == 0) {
+                uint32_t it = 0;
+                uint32_t tails = 0;   // odd CTA: parity of the next use of each stage's own barrier
+                int last_tail = -1;
+                // boxes and bytes of one K-block of CTA `r` of the pair
+                auto boxes_of = [&](int r) {
+                    const int half = mma_n<C>(p.n) / CTAS;
+                    const int n = max(0, min(half, p.n - r * half));
+                    return MODE == kDw ? (n + 63) / 64 : (n + C::kBoxRows - 1) / C::kBoxRows;
+                };
+                auto bytes_of = [&](int boxes) {
+                    return (uint32_t)(kABytes + boxes * (MODE == kDw ? 64 : C::kBoxRows) * kRowBytes);
+                };
+                while (!*abort && walk.next(p)) {
+                    if (MODE == kDw && p.rows == 0) continue;  // nothing to add up
+                    const int boxes = boxes_of(rank);
+                    const uint32_t bytes = bytes_of(boxes);
+                    const uint32_t all =
+                        CTAS == 2 ? bytes + bytes_of(boxes_of(1 - rank)) : bytes;
+                    const int b0 = rank * (mma_n<C>(p.n) / CTAS);  // first column of this CTA
+                    bool ok = true;
+                    for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
+                        const int i = it % kStages;
+                        if (it >= kStages && !tc::wait(&s.empty[i], (it / kStages - 1) & 1)) {
+                            timeout();
+                            ok = false;
+                            break;
+                        }
+                        uint8_t* sa = stage_ptr(i);
+                        uint8_t* sb = sa + kABytes;
+                        // copies complete on the barrier of the CTA that issues the
+                        // MMAs; a group's cut last K-block on each CTA's own, since
+                        // each clears rows of it first (the odd CTA's `full` barriers
+                        // have no other use)
+                        const bool tail = MODE == kDw && CTAS == 2 && p.rows - kb * C::BK < C::BK;
+                        uint32_t bar;
+                        if (CTAS == 1) {
+                            mbar_arrive_expect_tx(&s.full[i], bytes);
+                            bar = smem_addr(&s.full[i]);
+                        } else if (rank == 0) {
+                            mbar_arrive_expect_tx(&s.full[i], tail ? bytes : all);
+                            bar = tc::cluster_addr(&s.full[i], 0);
+                        } else if (tail) {
+                            mbar_arrive_expect_tx(&s.full[i], bytes);
+                            bar = tc::cluster_addr(&s.full[i], 1);
+                            tails ^= 1u << i;
+                            last_tail = i;
+                        } else {
+                            bar = tc::cluster_addr(&s.full[i], 0);
+                        }
+                        if constexpr (MODE == kFwd) {
+                            tc::tma_3d<CTAS>(sa, &amap, kb * C::BK, p.m0, p.e, bar);
+                        } else if constexpr (MODE == kDx) {
+                            tc::tma_3d<CTAS>(sa, &amap, p.m0, kb * C::BK, p.e, bar);
+                            tc::tma_3d<CTAS>(sa + kABytes / 2, &amap, p.m0 + 64, kb * C::BK, p.e,
+                                             bar);
+                        } else {
+                            const int r = p.row0 + kb * C::BK;
+                            tc::tma_2d<CTAS>(sa, &amap, p.m0, r, bar);
+                            tc::tma_2d<CTAS>(sa + kABytes / 2, &amap, p.m0 + 64, r, bar);
+                        }
+                        if constexpr (MODE == kDw) {
+                            for (int b = 0; b < boxes; ++b)
+                                tc::tma_2d<CTAS>(sb + b * 64 * kRowBytes, &bmap,
+                                                 p.col0 + b0 + b * 64, p.row0 + kb * C::BK, bar);
+                        } else {
+                            constexpr int kPer = C::kBigBox / C::kBoxRows;
+                            int b = 0;
+                            for (; b + kPer <= boxes; b += kPer)
+                                tc::tma_2d<CTAS>(sb + b * C::kBoxRows * kRowBytes, &bmap_big,
+                                                 kb * C::BK, p.row0 + b0 + b * C::kBoxRows, bar);
+                            for (; b < boxes; ++b)
+                                tc::tma_2d<CTAS>(sb + b * C::kBoxRows * kRowBytes, &bmap,
+                                                 kb * C::BK, p.row0 + b0 + b * C::kBoxRows, bar);
+                        }
+                    }
+                    if (!ok) break;
+                }
+                // after a timeout nobody consumes the stages: the copies in flight
+                // still end before this CTA does (those of the odd CTA complete on
+                // the even one's barriers)
+                if (*abort) {
+                    if (rank == 0)
+                        for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+                            tc::wait(&s.full[j % kStages], (j / kStages) & 1);
+                    else if (last_tail >= 0)
+                        tc::wait(&s.full[last_tail], (tails >> last_tail & 1) ^ 1);
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------- MMAs --------------------------------
+            constexpr uint32_t kAStep = C::kAMn ? 2048 / 16 : 2;  // one MMA along the reduction
+            constexpr uint32_t kBStep = C::kBMn ? 2048 / 16 : 2;
+            const uint64_t abase =
+                C::kAMn ? tc::desc_base(64 * kRowBytes, 1024) : tc::desc_base(0, 1024);
+            const uint64_t bbase =
+                C::kBMn ? tc::desc_base(64 * kRowBytes, 1024) : tc::desc_base(0, 1024);
+            // Clear the rows behind a group's end in this CTA's part of a stage
+            // (both operands: they may hold infinities), up to the next MMA step.
+            auto clear_tail = [&](int i, int valid) {
+                const int half = mma_n<C>(p.n) / CTAS;
+                const int n = max(0, min(half, p.n - (int)rank * half));
+                const int boxes = 2 + (n + 63) / 64;
+                const int chunks = ((valid + 15) / 16 * 16 - valid) * 8;
+                for (int b = 0; b < boxes; ++b)
+                    for (int j = lane; j < chunks; j += 32)
+                        *reinterpret_cast<uint4*>(stage_ptr(i) + b * 64 * kRowBytes +
+                                                  valid * kRowBytes + j * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+                __syncwarp();
+            };
+            uint32_t it = 0, ch = 0;
+            uint32_t tails = 0;  // parity of each stage's next cut last K-block
+            if (rank == 0) {
+                while (!*abort && walk.next(p)) {
+                    if (MODE == kDw && p.rows == 0) continue;
+                    const uint32_t id =
+                        tc::idesc(kBM * CTAS, mma_n<C>(p.n), FP8 ? 0 : 1, C::kAMn, C::kBMn);
+                    bool ok = true;
+                    for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
+                        const bool first = FP8 || (kb - p.kb0) % kChunk == 0;
+                        const uint32_t buf = ch & 1;
+                        if (first && ch >= 2) ok = tc::wait(&s.acc_empty[buf], (ch / 2 - 1) & 1);
+                        const int i = it % kStages;
+                        if (!ok || !tc::wait(&s.full[i], (it / kStages) & 1)) {
+                            timeout();
+                            ok = false;
+                            break;
+                        }
+                        int steps = 4;
+                        if constexpr (MODE == kDw) {
+                            const int valid = p.rows - kb * C::BK;
+                            if (valid < C::BK) {
+                                steps = (valid + 15) / 16;
+                                clear_tail(i, valid);
+                                if (CTAS == 2 &&
+                                    !tc::wait_cluster(&s.tail_ready[i], tails >> i & 1)) {
+                                    timeout();
+                                    ok = false;
+                                    break;
+                                }
+                                tails ^= 1u << i;
+                            }
+                        }
+                        tc::fence_after();
+                        const bool last =
+                            FP8 || kb + 1 == p.kb1 || (kb - p.kb0) % kChunk == kChunk - 1;
+                        if (lane == 0) {
+                            const uint32_t sa = smem_addr(stage_ptr(i));
+                            const uint64_t ad = tc::desc_at(abase, sa);
+                            const uint64_t bd = tc::desc_at(bbase, sa + kABytes);
+                            const uint32_t d = tmem + buf * C::BN;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < steps)
+                                    tc::mma<FP8, CTAS>(d, ad + k * kAStep, bd + k * kBStep, id,
+                                                       !first || k > 0);
+                            tc::commit<CTAS>(&s.empty[i]);
+                            if (last) tc::commit<CTAS>(&s.acc_full[buf]);
+                        }
+                        __syncwarp();
+                        if (last) ++ch;
+                    }
+                    if (!ok) break;
+                }
+            } else if (MODE == kDw) {
+                // the odd CTA of a pair only clears its part of cut last K-blocks
+                while (!*abort && walk.next(p)) {
+                    if (p.rows == 0) continue;
+                    it += p.kb1 - p.kb0;
+                    const int valid = p.rows - (p.kb1 - 1) * C::BK;
+                    if (valid >= C::BK) continue;
+                    const int i = (it - 1) % kStages;
+                    if (!tc::wait(&s.full[i], tails >> i & 1)) {
                         timeout();
-                        ok = false;
                         break;
                     }
-                    uint8_t* sa = stage_ptr(i);
-                    uint8_t* sb = sa + kABytes;
-                    mbar_arrive_expect_tx(&s.full[i], bytes);
-                    if constexpr (MODE == kFwd) {
-                        tc::tma_3d(sa, &amap, kb * C::BK, p.m0, p.e, &s.full[i]);
-                    } else if constexpr (MODE == kDx) {
-                        tc::tma_3d(sa, &amap, p.m0, kb * C::BK, p.e, &s.full[i]);
-                        tc::tma_3d(sa + kABytes / 2, &amap, p.m0 + 64, kb * C::BK, p.e, &s.full[i]);
-                    } else {
-                        const int r = p.row0 + kb * C::BK;
-                        tc::tma_2d(sa, &amap, p.m0, r, &s.full[i]);
-                        tc::tma_2d(sa + kABytes / 2, &amap, p.m0 + 64, r, &s.full[i]);
-                    }
-                    if constexpr (MODE == kDw) {
-                        for (int b = 0; b < boxes; ++b)
-                            tc::tma_2d(sb + b * 64 * kRowBytes, &bmap, p.col0 + b * 64,
-                                       p.row0 + kb * C::BK, &s.full[i]);
-                    } else {
-                        for (int b = 0; b < boxes; ++b)
-                            tc::tma_2d(sb + b * C::kBoxRows * kRowBytes, &bmap, kb * C::BK,
-                                       p.row0 + b * C::kBoxRows, &s.full[i]);
-                    }
+                    tails ^= 1u << i;
+                    clear_tail(i, valid);
+                    if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&s.tail_ready[i], 0));
                 }
-                if (!ok) break;
             }
-            // after a timeout nobody consumes the stages: the copies in flight
-            // still end before this CTA does
-            if (*abort)
-                for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-                    mbar_wait(&s.full[j % kStages], (j / kStages) & 1);
-        }
-    } else if (warp == 1) {
-        // -------------------------------- MMAs ---------------------------------
-        const uint64_t abase = C::kAMn ? tc::desc_base(64 * kRowBytes, 1024) : tc::desc_base(0, 1024);
-        const uint64_t bbase = C::kBMn ? tc::desc_base(64 * kRowBytes, 1024) : tc::desc_base(0, 1024);
-        constexpr uint32_t kAStep = C::kAMn ? 2048 / 16 : 2;  // one MMA along the reduction
-        constexpr uint32_t kBStep = C::kBMn ? 2048 / 16 : 2;
-        uint32_t it = 0, ch = 0;
-        while (!*abort && walk.next(p)) {
-            if (MODE == kDw && p.rows == 0) continue;
-            const uint32_t id = tc::idesc(kBM, mma_n(p.n), FP8 ? 0 : 1, C::kAMn, C::kBMn);
-            bool ok = true;
-            for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                const bool first = FP8 || (kb - p.kb0) % kChunk == 0;
-                const uint32_t buf = ch & 1;
-                if (first && ch >= 2) {
-                    if (!mbar_wait(&s.acc_empty[buf], (ch / 2 - 1) & 1)) ok = false;
-                }
-                const int i = it % kStages;
-                if (!ok || !mbar_wait(&s.full[i], (it / kStages) & 1)) {
-                    timeout();
-                    ok = false;
-                    break;
-                }
-                int steps = 4;
-                if constexpr (MODE == kDw) {
-                    // the group's last K-block: rows of the next group behind
-                    // its end are cleared (in both operands: they may hold
-                    // infinities), whole MMA steps of them are left out
-                    const int valid = p.rows - kb * C::BK;
-                    if (valid < C::BK) {
-                        steps = (valid + 15) / 16;
-                        const int boxes = 2 + (p.n + 63) / 64;
-                        const int clear = (steps * 16 - valid) * 8;
-                        uint8_t* sa = stage_ptr(i);
-                        for (int b = 0; b < boxes; ++b)
-                            for (int j = lane; j < clear; j += 32)
-                                *reinterpret_cast<uint4*>(sa + b * 64 * kRowBytes +
-                                                          valid * kRowBytes + j * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        fence_proxy_async();
-                        __syncwarp();
-                    }
-                }
-                tc::fence_after();
-                const bool last = FP8 || kb + 1 == p.kb1 || (kb - p.kb0) % kChunk == kChunk - 1;
-                if (lane == 0) {
-                    const uint32_t sa = smem_addr(stage_ptr(i));
-                    const uint64_t ad = tc::desc_at(abase, sa);
-                    const uint64_t bd = tc::desc_at(bbase, sa + kABytes);
-                    const uint32_t d = tmem + buf * C::BN;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < steps)
-                            tc::mma<FP8, 1>(d, ad + k * kAStep, bd + k * kBStep, id,
-                                            !first || k > 0);
-                    tc::commit(&s.empty[i]);
-                    if (last) tc::commit(&s.acc_full[buf]);
-                }
-                __syncwarp();
-                if (last) ++ch;
-            }
-            if (!ok) break;
-        }
-    } else if (warp < kEpiWarp0) {
-        // ---------------- fp8: products of the two scales, per column -------------
-        if constexpr (FP8) {
+        } else if constexpr (FP8) {
+            // ------------- fp8: products of the two scales, per column --------------
             const int KB = (a.red + C::BK - 1) / C::BK;
+            const int w_tiles = (a.M + kBM - 1) / kBM;
             uint32_t ch = 0;
             while (!*abort && walk.next(p)) {
-                const float* wsc = a.ws + ((int64_t)p.e * walk.m_tiles + p.m0 / kBM) * KB;
+                // (an odd CTA past the last weight rows computes nothing that is stored)
+                const int wt = min(p.m0 / kBM, w_tiles - 1);
+                const float* wsc = a.ws + ((int64_t)p.e * w_tiles + wt) * KB;
                 bool ok = true;
                 for (int kb = p.kb0; kb < p.kb1; ++kb, ++ch) {
                     if ((int)(ch & 1) != warp - 2) continue;  // the two warps alternate
@@ -459,7 +599,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
 #pragma unroll
                     for (int j = 0; j < C::BN / 32; ++j)
                         v[j] = j * 32 + lane < p.n ? __ldg(xs + j * 32 + lane) * sw : 0.f;
-                    if (ch >= kScaleBufs && !mbar_wait(&s.sc_empty[b], (ch / kScaleBufs - 1) & 1)) {
+                    if (ch >= kScaleBufs && !tc::wait(&s.sc_empty[b], (ch / kScaleBufs - 1) & 1)) {
                         if (lane == 0) timeout();
                         ok = false;
                         break;
@@ -474,54 +614,48 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
         }
     } else {
         // ------------------------------ epilogue ---------------------------------
+        if constexpr (kSplitRegs) tc::regs_inc<216>();
         const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
-        const int mrow = q * 32 + lane;       // row of the tile
-        const int c0 = half * C::kAcc;        // this thread's columns: [c0, c0 + kAcc)
-        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
+        const int mrow = q * 32 + lane;       // row of this CTA's part of the tile
+        uint8_t* stage_out = store0 + (warp - kEpiWarp0) * kStoreBytes;
+        const uint32_t acc_empty[2] = {
+            CTAS == 2 ? tc::cluster_addr(&s.acc_empty[0], 0) : smem_addr(&s.acc_empty[0]),
+            CTAS == 2 ? tc::cluster_addr(&s.acc_empty[1], 0) : smem_addr(&s.acc_empty[1])};
         uint32_t ch = 0;
         while (!*abort && walk.next(p)) {
+            // the two warps of a lane quarter share the columns evenly
+            // (kDw: in whole stores of 64 bf16 values)
+            constexpr int kShare = MODE == kDw ? 64 : 32;
+            const int hn = (p.n + 2 * kShare - 1) / (2 * kShare) * kShare;
+            const int c0 = half * hn;                       // first column of this thread
+            const int nc = max(0, min(p.n - c0, hn));       // and how many
+            const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
             float acc[C::kAcc];
 #pragma unroll
             for (int j = 0; j < C::kAcc; ++j) acc[j] = 0.f;
             bool ok = true;
-            if (!(MODE == kDw && p.rows == 0)) {
+            if (MODE == kDw && p.rows == 0) {
+                if (a.accumulate) continue;  // nothing to add
+            } else {
                 const int n_ch = FP8 ? p.kb1 - p.kb0 : (p.kb1 - p.kb0 + kChunk - 1) / kChunk;
                 for (int i = 0; i < n_ch; ++i, ++ch) {
                     const uint32_t buf = ch & 1, sb = ch % kScaleBufs;
-                    if (!mbar_wait(&s.acc_full[buf], (ch / 2) & 1) ||
-                        (FP8 && !mbar_wait(&s.sc_full[sb], (ch / kScaleBufs) & 1))) {
+                    if (!tc::wait(&s.acc_full[buf], (ch / 2) & 1) ||
+                        (FP8 && !tc::wait(&s.sc_full[sb], (ch / kScaleBufs) & 1))) {
                         if (lane == 0) timeout();
                         ok = false;
                         break;
                     }
                     tc::fence_after();
-#pragma unroll
-                    for (int j0 = 0; j0 < C::kAcc; j0 += 16) {
-                        if (c0 + j0 < p.n) {
-                            uint32_t v[16];
-                            tc::ld16(tq + buf * C::BN + j0, v);
-                            tc::ld_wait(v);
-                            if constexpr (FP8) {
-                                const float4* sc =
-                                    reinterpret_cast<const float4*>(scale0 + sb * C::BN + c0 + j0);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const float4 f = sc[j];
-                                    acc[j0 + 4 * j] += __uint_as_float(v[4 * j]) * f.x;
-                                    acc[j0 + 4 * j + 1] += __uint_as_float(v[4 * j + 1]) * f.y;
-                                    acc[j0 + 4 * j + 2] += __uint_as_float(v[4 * j + 2]) * f.z;
-                                    acc[j0 + 4 * j + 3] += __uint_as_float(v[4 * j + 3]) * f.w;
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) acc[j0 + j] += __uint_as_float(v[j]);
-                            }
-                        }
-                    }
+                    const uint32_t src = tq + buf * C::BN;
+                    const float* sc = scale0 + sb * C::BN + c0;
+                    if (nc == C::kAcc) drain<C, FP8, true>(src, sc, nc, acc);
+                    else if (nc > 0) drain<C, FP8, false>(src, sc, nc, acc);
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&s.acc_empty[buf]);
+                        if (CTAS == 2) tc::arrive_cluster(acc_empty[buf]);
+                        else mbar_arrive(&s.acc_empty[buf]);
                         if (FP8) mbar_arrive(&s.sc_empty[sb]);
                     }
                 }
@@ -529,20 +663,25 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
             if (!ok) break;
 
             if (p.kb1 - p.kb0 < p.kb) {
-                // a cut tile: leave the partial sums; the last of its ranges adds them
-                const long long rng = walk.range();
-                const int c_first = (int)(p.step / rng);
-                const int c_last = (int)((p.step + p.kb - 1) / rng);
-                float* mine = a.part + ((int64_t)blockIdx.x * 2 + (p.kb0 == 0)) * (kBM * C::BN);
+                // a cut tile: leave the partial sums; the last of its ranges adds
+                // them, in the order of the ranges
+                const int c_first = p.step / s.range;
+                const int c_last = (p.step + p.kb - 1) / s.range;
+                constexpr int kPart = kBM * C::BN;
+                auto part_of = [&](int worker, bool head) {
+                    return a.part + (((int64_t)worker * 2 + head) * CTAS + rank) * kPart +
+                           c0 * kBM + mrow;
+                };
+                float* mine = part_of(walk.worker(), p.kb0 == 0);
 #pragma unroll
                 for (int j = 0; j < C::kAcc; ++j)
-                    if (c0 + j < p.n) __stcg(mine + (c0 + j) * kBM + mrow, acc[j]);
+                    if (j < nc) __stcg(mine + j * kBM, acc[j]);
                 __threadfence();
                 named_barrier(1, kEpiWarps * 32);
                 if (warp == kEpiWarp0 && lane == 0) {
-                    const int before = atomicAdd(a.counters + c_first, 1);
-                    s.last = before == c_last - c_first;
-                    if (s.last) a.counters[c_first] = 0;
+                    int* count = a.counters + c_first * CTAS + rank;
+                    s.last = atomicAdd(count, 1) == c_last - c_first;
+                    if (s.last) *count = 0;
                 }
                 named_barrier(1, kEpiWarps * 32);
                 if (!*const_cast<volatile int*>(&s.last)) continue;
@@ -550,84 +689,116 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
 #pragma unroll
                 for (int j = 0; j < C::kAcc; ++j) acc[j] = 0.f;
                 for (int c = c_first; c <= c_last; ++c) {
-                    const float* src = a.part + ((int64_t)c * 2 + (c == c_first)) * (kBM * C::BN);
+                    const float* src = part_of(c, c == c_first);
 #pragma unroll
-                    for (int j = 0; j < C::kAcc; ++j)
-                        if (c0 + j < p.n) acc[j] += __ldcg(src + (c0 + j) * kBM + mrow);
+                    for (int j0 = 0; j0 < C::kAcc; j0 += 16) {
+                        if (j0 >= nc) break;
+                        float f[16];  // all loads of a group in flight (its padding is read too)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[j] = __ldcg(src + (j0 + j) * kBM);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[j0 + j] += f[j];
+                    }
                 }
             }
 
             const int m = p.m0 + mrow;
-            if (m >= a.M) {
-                // a row of the last M tile that does not exist
-            } else if constexpr (MODE == kDw) {
-                // a thread's columns are consecutive in its row of dw; columns
-                // come in whole vectors of 8
-                const int64_t o = ((int64_t)p.e * a.M + m) * a.cols + p.col0;
+            if constexpr (MODE == kDw) {
+                // 32 rows x 128 bytes at a time through shared memory to a tensor
+                // store, which leaves out what lies outside dw
+                if (!(a.accumulate && a.out_bf16)) {
+                    const int per = a.out_bf16 ? 64 : 32;   // columns per store
 #pragma unroll
-                for (int j0 = 0; j0 < C::kAcc; j0 += 8) {
-                    if (c0 + j0 >= p.n) continue;
-                    float* v = acc + j0;
-                    if (a.out_bf16) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o +
-                                                              c0 + j0);
-                        uint32_t u[4];
-                        if (a.accumulate) {
-                            const uint4 old = *dst;
-                            const uint32_t w[4] = {old.x, old.y, old.z, old.w};
+                    for (int g = 0; g < C::kAcc / 32; ++g) {
+                        if (g * 32 >= nc || p.m0 + q * 32 >= a.M) break;
+                        // bf16: two groups of 32 columns fill one store
+                        if (!a.out_bf16 || (g & 1) == 0) {
+                            if (lane == 0) tc::store_read_wait();
+                            __syncwarp();
+                        }
+                        if (a.out_bf16) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                v[2 * j] += __uint_as_float(w[j] << 16);
-                                v[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
-                            }
-                        }
+                                uint32_t u[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                            u[j] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                        *dst = make_uint4(u[0], u[1], u[2], u[3]);
-                    } else {
-                        float4* dst =
-                            reinterpret_cast<float4*>(static_cast<float*>(a.out) + o + c0 + j0);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float4 f = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2],
-                                                   v[4 * j + 3]);
-                            if (a.accumulate) {
-                                const float4 old = dst[j];
-                                f.x += old.x; f.y += old.y; f.z += old.z; f.w += old.w;
+                                for (int i = 0; i < 4; ++i) {
+                                    const float* f = acc + g * 32 + 8 * j + 2 * i;
+                                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[0], f[1]);
+                                    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+                                }
+                                const int chunk = (g & 1) * 4 + j;
+                                *reinterpret_cast<uint4*>(stage_out + lane * 128 +
+                                                          ((chunk ^ (lane & 7)) << 4)) =
+                                    make_uint4(u[0], u[1], u[2], u[3]);
                             }
-                            dst[j] = f;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                *reinterpret_cast<float4*>(stage_out + lane * 128 +
+                                                           ((j ^ (lane & 7)) << 4)) =
+                                    make_float4(acc[g * 32 + 4 * j], acc[g * 32 + 4 * j + 1],
+                                                acc[g * 32 + 4 * j + 2], acc[g * 32 + 4 * j + 3]);
+                        }
+                        if (!a.out_bf16 || (g & 1) || (g + 1) * 32 >= nc) {
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0)
+                                tc::tma_store_3d(&omap, stage_out,
+                                                 p.col0 + c0 + g * 32 / per * per, p.m0 + q * 32,
+                                                 p.e, a.accumulate);
                         }
                     }
+                } else if (m < a.M) {
+                    // added to bf16 values: one rounding of the whole sum
+                    uint4* dst = reinterpret_cast<uint4*>(
+                        static_cast<uint16_t*>(a.out) + ((int64_t)p.e * a.M + m) * a.cols + p.col0 +
+                        c0);
+#pragma unroll
+                    for (int j0 = 0; j0 < C::kAcc; j0 += 8) {
+                        if (j0 >= nc) break;  // columns come in whole vectors of 8
+                        const uint4 old = dst[j0 / 8];
+                        const uint32_t w[4] = {old.x, old.y, old.z, old.w};
+                        uint32_t u[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float* f = acc + j0 + 2 * j;
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(
+                                f[0] + __uint_as_float(w[j] << 16),
+                                f[1] + __uint_as_float(w[j] & 0xFFFF0000u));
+                            u[j] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        dst[j0 / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
                 }
-            } else {
+            } else if (m < a.M) {
                 // a warp writes 32 consecutive values of one row at a time
-                const int64_t o = (int64_t)p.row0 * a.M + m;
+                const int64_t o = (int64_t)(p.row0 + c0) * a.M + m;
                 if (a.out_bf16) {
                     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + o;
 #pragma unroll
                     for (int j = 0; j < C::kAcc; ++j)
-                        if (c0 + j < p.n) dst[(int64_t)(c0 + j) * a.M] = __float2bfloat16_rn(acc[j]);
+                        if (j < nc) dst[(int64_t)j * a.M] = __float2bfloat16_rn(acc[j]);
                 } else {
                     float* dst = static_cast<float*>(a.out) + o;
 #pragma unroll
                     for (int j = 0; j < C::kAcc; ++j)
-                        if (c0 + j < p.n) dst[(int64_t)(c0 + j) * a.M] = acc[j];
+                        if (j < nc) dst[(int64_t)j * a.M] = acc[j];
                 }
             }
             __syncwarp();
         }
+        if (MODE == kDw && lane == 0) tc::store_wait();
     }
 
+    __syncwarp();
     tc::fence_before();
     __syncthreads();
+    // a pair ends together: the even CTA's MMAs read the odd one's memory, the
+    // odd one's epilogue arrives on the even one's barriers
+    if constexpr (CTAS == 2) tc::cluster_sync();
     if (warp == 2) {
         tc::fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(C::kTmemCols)
-                     : "memory");
+        tc::dealloc<CTAS>(tmem, C::kTmemCols);
     }
 }
 
@@ -647,49 +818,70 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-// [outer][rows][inner] elements (bf16 or bytes), boxes of 128 bytes x box_rows
-// with the 128-byte swizzle; what lies outside reads as zero.
-bool encode_operand(CUtensorMap* m, bool fp8, const void* base, int inner, int64_t rows, int outer,
-                    int box_rows) {
+enum Type { kBytes, kBf16, kF32 };
+
+// [outer][rows][inner] elements (outer 0: two dimensions), boxes of 128 bytes x
+// box_rows with the 128-byte swizzle; what lies outside reads as zero.
+bool encode(CUtensorMap* m, Type type, const void* base, int inner, int64_t rows, int outer,
+            int box_rows) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
-    const uint64_t size = fp8 ? 1 : 2;
+    const uint64_t size = type == kBytes ? 1 : type == kBf16 ? 2 : 4;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
     const cuuint64_t strides[2] = {inner * size, inner * size * (uint64_t)rows};
     const cuuint32_t box[3] = {(cuuint32_t)(kRowBytes / size), (cuuint32_t)box_rows, 1};
     const cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-               outer > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
+    const CUtensorMapDataType dt = type == kBytes  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : type == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return enc(m, dt, outer > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool FP8, int BN>
+template <int MODE, bool FP8, int BN, int CTAS>
 coli_status launch_mm(const void* A, const void* B, const MmArgs& a, int N, int K, cudaStream_t st) {
-    using C = Cfg<MODE, FP8, BN>;
-    CUtensorMap amap, bmap;
+    using C = Cfg<MODE, FP8, BN, CTAS>;
+    const Type in = FP8 ? kBytes : kBf16;
+    CUtensorMap amap, bmap, big, omap;
     bool ok;
-    if constexpr (MODE == kDw)
-        ok = encode_operand(&amap, false, A, N, a.R, 0, 64) &&
-             encode_operand(&bmap, false, B, K, a.R, 0, 64);
-    else
-        ok = encode_operand(&amap, FP8, A, K, N, a.E, MODE == kFwd ? kBM : 64) &&
-             encode_operand(&bmap, FP8, B, MODE == kFwd ? K : N, a.R, 0, C::kBoxRows);
+    if constexpr (MODE == kDw) {
+        ok = encode(&amap, in, A, N, a.R, 0, 64) && encode(&bmap, in, B, K, a.R, 0, 64) &&
+             encode(&omap, a.out_bf16 ? kBf16 : kF32, a.out, K, N, a.E, 32);
+        big = bmap;  // not used
+    } else {
+        ok = encode(&amap, in, A, K, N, a.E, MODE == kFwd ? kBM : 64) &&
+             encode(&bmap, in, B, MODE == kFwd ? K : N, a.R, 0, C::kBoxRows) &&
+             encode(&big, in, B, MODE == kFwd ? K : N, a.R, 0, C::kBigBox);
+        omap = amap;  // not used
+    }
     if (!ok) return COLI_ERR_CUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return COLI_ERR_CUDA;
-    constexpr int smem = 1024 + stage_count<C, FP8>() * C::kStage + scale_bytes<C, FP8>() +
-                         kSharedBytes;
-    static_assert(smem <= kSmemMax && stage_count<C, FP8>() >= 3, "shared memory");
-    auto kernel = grouped_mm_kernel<MODE, FP8, BN>;
+    constexpr int smem = fixed_smem<C>() + stage_count<C>() * C::kStage;
+    static_assert(smem <= kSmemMax && stage_count<C>() >= 4, "shared memory");
+    auto kernel = grouped_mm_kernel<MODE, FP8, BN, CTAS>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
         return COLI_ERR_CUDA;
-    const cudaError_t err =
-        launch_serialized(kernel, dim3(std::min(sms, kMaxGrid)), dim3(kThreads), smem, st, amap,
-                          bmap, a);
+    const int grid = std::max(CTAS, std::min(sms, kMaxGrid) / CTAS * CTAS);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CTAS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CTAS == 2 ? 2 : 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, amap, bmap, big, omap, a);
     return err == cudaSuccess ? COLI_OK : COLI_ERR_CUDA;
 }
 
@@ -754,8 +946,8 @@ coli_status coli_moe_grouped_mm(int32_t R, int32_t E, int32_t N, int32_t K, cons
     if (s != COLI_OK) return s;
     const MmArgs a = make_mm_args(offsets, R, E, N, K, out, out_dtype, ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return narrow(R, E) ? launch_mm<kFwd, false, 64>(w_bf16, x_bf16, a, N, K, st)
-                        : launch_mm<kFwd, false, 256>(w_bf16, x_bf16, a, N, K, st);
+    return narrow(R, E) ? launch_mm<kFwd, false, 64, 1>(w_bf16, x_bf16, a, N, K, st)
+                        : launch_mm<kFwd, false, 256, 2>(w_bf16, x_bf16, a, N, K, st);
 }
 
 coli_status coli_moe_grouped_mm_dx(int32_t R, int32_t E, int32_t N, int32_t K, const void* dy_bf16,
@@ -768,8 +960,8 @@ coli_status coli_moe_grouped_mm_dx(int32_t R, int32_t E, int32_t N, int32_t K, c
     if (s != COLI_OK) return s;
     const MmArgs a = make_mm_args(offsets, R, E, K, N, dx, dx_dtype, ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return narrow(R, E) ? launch_mm<kDx, false, 64>(w_bf16, dy_bf16, a, N, K, st)
-                        : launch_mm<kDx, false, 256>(w_bf16, dy_bf16, a, N, K, st);
+    return narrow(R, E) ? launch_mm<kDx, false, 64, 1>(w_bf16, dy_bf16, a, N, K, st)
+                        : launch_mm<kDx, false, 256, 2>(w_bf16, dy_bf16, a, N, K, st);
 }
 
 coli_status coli_moe_grouped_mm_dw(int32_t R, int32_t E, int32_t N, int32_t K, const void* dy_bf16,
@@ -790,7 +982,7 @@ coli_status coli_moe_grouped_mm_dw(int32_t R, int32_t E, int32_t N, int32_t K, c
     MmArgs a = make_mm_args(offsets, R, E, N, 0, dw, dw_dtype, ws);
     a.cols = K;
     a.accumulate = accumulate != 0;
-    return launch_mm<kDw, false, 256>(dy_bf16, x_bf16, a, N, K, st);
+    return launch_mm<kDw, false, 256, 2>(dy_bf16, x_bf16, a, N, K, st);
 }
 
 coli_status coli_moe_fp8_grouped_mm(int32_t R, int32_t E, int32_t N, int32_t K, const uint8_t* xq,
@@ -807,8 +999,8 @@ coli_status coli_moe_fp8_grouped_mm(int32_t R, int32_t E, int32_t N, int32_t K, 
     a.xs = x_scale;
     a.ws = w_scale;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return narrow(R, E) ? launch_mm<kFwd, true, 64>(wq, xq, a, N, K, st)
-                        : launch_mm<kFwd, true, 256>(wq, xq, a, N, K, st);
+    return narrow(R, E) ? launch_mm<kFwd, true, 64, 1>(wq, xq, a, N, K, st)
+                        : launch_mm<kFwd, true, 256, 1>(wq, xq, a, N, K, st);
 }
 
 }  // extern "C"
