@@ -47,7 +47,8 @@
 namespace coli {
 namespace {
 
-enum Mode { kFwd = 0, kDx = 1, kDw = 2 };
+// kFwdRows: kFwd with the rows as M and the weight rows as N
+enum Mode { kFwd = 0, kDx = 1, kDw = 2, kFwdRows = 3 };
 
 constexpr int kBM = 128;               // M per CTA
 constexpr int kRowBytes = 128;         // bytes of one operand row (or column) per stage
@@ -60,6 +61,7 @@ constexpr int kChunk = 8;              // bf16 K-blocks per accumulator chain
 constexpr int kScaleBufs = 4;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kMinRange = 4;           // K-blocks of a range of the last wave, at least
+constexpr int kBand = 8;
 constexpr int kStoreBytes = 32 * 128;  // kDw: staging of one warp's stores
 
 struct MmArgs {
@@ -84,16 +86,19 @@ template <int MODE, bool FP8, int BN_, int CTAS_>
 struct Cfg {
     static constexpr int BN = BN_, CTAS = CTAS_;
     static constexpr int BK = FP8 ? 128 : 64;              // reduction per stage
-    static constexpr int kBoxRows = BN == 256 ? 32 : 16;   // rows per B tensor copy, and
-    static constexpr int kBigBox = BN == 256 ? 128 : 64;   // rows of the copies of whole parts
+    static constexpr bool kRows = MODE == kFwdRows;
+    // rows per B tensor copy, and of the copies of whole parts
+    static constexpr int kBoxRows = kRows ? 128 : BN == 256 ? 32 : 16;
+    static constexpr int kBigBox = BN == 256 ? 128 : 64;
     static constexpr int kBBytes = BN / CTAS * kRowBytes;
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kNGrain = 16 * CTAS;              // MMA N in multiples of this
-    static constexpr bool kAMn = MODE != kFwd;
+    static constexpr bool kAMn = MODE == kDx || MODE == kDw;
     static constexpr bool kBMn = MODE == kDw;
     static constexpr int kAcc = BN / 2;                    // accumulators per epilogue thread
-    static constexpr int kScaleBytes = FP8 ? kScaleBufs * BN * 4 : 0;
+    static constexpr bool kColScale = FP8 && !kRows;       // scales per column, in shared memory
+    static constexpr int kScaleBytes = kColScale ? kScaleBufs * BN * 4 : 0;
     static constexpr int kStoreStage = MODE == kDw ? kEpiWarps * kStoreBytes : 0;
 };
 
@@ -124,8 +129,8 @@ constexpr int stage_count() {
 // A piece of work: K-blocks [kb0, kb1) of one tile.
 struct Piece {
     int e, m0;           // expert; first M row of this CTA
-    int row0, rows;      // kFwd, kDx: the tile's rows; kDw: the group's
-    int col0;            // kDw: first column
+    int row0, rows;      // the tile's rows; kDw: the group's
+    int col0;            // kDw, kFwdRows: first column
     int n;               // valid columns of the MMA N dimension
     int kb0, kb1, kb;    // of kb
     int step;            // of the tile's first K-block in the last wave's sequence
@@ -145,12 +150,16 @@ struct Walk {
     static __device__ __forceinline__ int worker() { return blockIdx.x / C::CTAS; }
     static __device__ __forceinline__ int workers() { return gridDim.x / C::CTAS; }
     static __device__ __forceinline__ int rank() { return blockIdx.x % C::CTAS; }
+    // tiles of one group (kDw) or of one row tile of it
     static __device__ __forceinline__ int m_tiles(const MmArgs& a) {
-        return (a.M + kBM * C::CTAS - 1) / (kBM * C::CTAS);
+        const int per = C::kRows ? C::BN : kBM * C::CTAS;
+        return (a.M + per - 1) / per;
     }
     static __device__ __forceinline__ int c_tiles(const MmArgs& a) {
         return MODE == kDw ? (a.cols + C::BN - 1) / C::BN : 1;
     }
+    // rows of a row tile, at most
+    static constexpr int kTileRows = C::kRows ? kBM * C::CTAS : C::BN;
     static __device__ __forceinline__ int group_kb(const MmArgs& a, int e) {
         if (MODE != kDw) return (a.red + C::BK - 1) / C::BK;
         const int rows = __ldg(a.offsets + e + 1) - __ldg(a.offsets + e);
@@ -199,14 +208,27 @@ struct Walk {
             p.row0 = off;
             p.rows = rows;
         } else {
-            // a group's rows are shared evenly by its row tiles (16-row grain)
-            const int nt = s.tile0[e + 1] - s.tile0[e];
-            const int bn = ((rows + nt - 1) / nt + 15) & ~15;
-            const int i = t % nt * bn;
-            p.m0 = (t / nt * C::CTAS + rank()) * kBM;
-            p.col0 = 0;
-            p.row0 = off + i;
-            p.rows = p.n = max(0, min(bn, rows - i));
+            // bands of kBand row tiles, the row tiles of a band fastest: what
+            // the workers have in hand at a time is few strips of both operands
+            const int nt = s.tile0[e + 1] - s.tile0[e], mt = m_tiles(a);
+            const int band = t / (kBand * mt), in = t - band * kBand * mt;
+            const int bw = min(kBand, nt - band * kBand);
+            const int ti = band * kBand + in % bw, tm = in / bw;
+            if (C::kRows) {
+                const int i = (ti * C::CTAS + rank()) * kBM;
+                p.row0 = off + i;
+                p.rows = max(0, min(kBM, rows - i));
+                p.m0 = 0;
+                p.col0 = tm * C::BN;
+                p.n = min(C::BN, a.M - p.col0);
+            } else {
+                // a group's rows are shared evenly by its row tiles (16-row grain)
+                const int bn = ((rows + nt - 1) / nt + 15) & ~15, i = ti * bn;
+                p.m0 = (tm * C::CTAS + rank()) * kBM;
+                p.col0 = 0;
+                p.row0 = off + i;
+                p.rows = p.n = max(0, min(bn, rows - i));
+            }
         }
     }
     __device__ __forceinline__ bool next(Piece& p) {
@@ -240,11 +262,13 @@ __device__ __forceinline__ int mma_n(int n) {
     return (max(n, 1) + C::kNGrain - 1) / C::kNGrain * C::kNGrain;
 }
 
-// Add one accumulator's columns (times their scales) to a thread's sums.  The
+// Add one accumulator's columns (times their scales: `sc` per column or `one`
+// for all) to a thread's sums.  The
 // loads of 16 columns run under the sums of the 16 before; a whole tile's loop
 // has no branches, so its instructions interleave.
 template <class C, bool FP8, bool WHOLE>
-__device__ __forceinline__ void drain(uint32_t src, const float* sc, int nc, float (&acc)[C::kAcc]) {
+__device__ __forceinline__ void drain(uint32_t src, const float* sc, float one, int nc,
+                                      float (&acc)[C::kAcc]) {
     constexpr int kGroups = C::kAcc / 16;
     uint32_t v[2][16];
     tc::ld16(src, v[0]);
@@ -252,7 +276,7 @@ __device__ __forceinline__ void drain(uint32_t src, const float* sc, int nc, flo
     for (int g = 0; g < kGroups; ++g) {
         if (!WHOLE && g * 16 >= nc) break;
         float4 f[4];
-        if constexpr (FP8) {
+        if constexpr (C::kColScale) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = reinterpret_cast<const float4*>(sc + g * 16)[j];
         }
@@ -263,7 +287,12 @@ __device__ __forceinline__ void drain(uint32_t src, const float* sc, int nc, flo
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float* d = acc + g * 16 + 4 * j;
-            if constexpr (FP8) {
+            if constexpr (C::kRows) {
+                d[0] += __uint_as_float(w[4 * j]) * one;
+                d[1] += __uint_as_float(w[4 * j + 1]) * one;
+                d[2] += __uint_as_float(w[4 * j + 2]) * one;
+                d[3] += __uint_as_float(w[4 * j + 3]) * one;
+            } else if constexpr (C::kColScale) {
                 d[0] += __uint_as_float(w[4 * j]) * f[j].x;
                 d[1] += __uint_as_float(w[4 * j + 1]) * f[j].y;
                 d[2] += __uint_as_float(w[4 * j + 2]) * f[j].z;
@@ -339,7 +368,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                     v[i] = 1;
                     w[i] = max(1, (hi - lo + C::BK - 1) / C::BK);
                 } else {
-                    v[i] = (hi - lo + C::BN - 1) / C::BN;
+                    constexpr int kTileRows = Walk<MODE, C>::kTileRows;
+                    v[i] = (hi - lo + kTileRows - 1) / kTileRows;
                     w[i] = v[i] * ((a.red + C::BK - 1) / C::BK);
                 }
             }
@@ -449,6 +479,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                         }
                         if constexpr (MODE == kFwd) {
                             tc::tma_3d<CTAS>(sa, &amap, kb * C::BK, p.m0, p.e, bar);
+                        } else if constexpr (C::kRows) {
+                            tc::tma_2d<CTAS>(sa, &amap, kb * C::BK, p.row0, bar);
                         } else if constexpr (MODE == kDx) {
                             tc::tma_3d<CTAS>(sa, &amap, p.m0, kb * C::BK, p.e, bar);
                             tc::tma_3d<CTAS>(sa + kABytes / 2, &amap, p.m0 + 64, kb * C::BK, p.e,
@@ -462,6 +494,11 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                             for (int b = 0; b < boxes; ++b)
                                 tc::tma_2d<CTAS>(sb + b * 64 * kRowBytes, &bmap,
                                                  p.col0 + b0 + b * 64, p.row0 + kb * C::BK, bar);
+                        } else if constexpr (C::kRows) {
+                            for (int b = 0; b < boxes; ++b)
+                                tc::tma_3d<CTAS>(sb + b * C::kBoxRows * kRowBytes, &bmap,
+                                                 kb * C::BK, p.col0 + b0 + b * C::kBoxRows, p.e,
+                                                 bar);
                         } else {
                             constexpr int kPer = C::kBigBox / C::kBoxRows;
                             int b = 0;
@@ -577,10 +614,10 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                     }
                     tails ^= 1u << i;
                     clear_tail(i, valid);
-                    if (lane == 0) tc::arrive_cluster(tc::cluster_addr(&s.tail_ready[i], 0));
+                    if (lane == 0) tc::arrive_release_cluster(tc::cluster_addr(&s.tail_ready[i], 0));
                 }
             }
-        } else if constexpr (FP8) {
+        } else if constexpr (C::kColScale) {
             // ------------- fp8: products of the two scales, per column --------------
             const int KB = (a.red + C::BK - 1) / C::BK;
             const int w_tiles = (a.M + kBM - 1) / kBM;
@@ -624,9 +661,10 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
         uint32_t ch = 0;
         while (!*abort && walk.next(p)) {
             // the two warps of a lane quarter share the columns evenly
-            // (kDw: in whole stores of 64 bf16 values)
+            // (kDw: in whole stores of 64 bf16 values; kFwdRows: the columns of one
+            // weight scale each)
             constexpr int kShare = MODE == kDw ? 64 : 32;
-            const int hn = (p.n + 2 * kShare - 1) / (2 * kShare) * kShare;
+            const int hn = C::kRows ? 128 : (p.n + 2 * kShare - 1) / (2 * kShare) * kShare;
             const int c0 = half * hn;                       // first column of this thread
             const int nc = max(0, min(p.n - c0, hn));       // and how many
             const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
@@ -637,11 +675,29 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
             if (MODE == kDw && p.rows == 0) {
                 if (a.accumulate) continue;  // nothing to add
             } else {
+                // kFwdRows: this thread's row has one scale per K-block, its columns
+                // one weight scale; both are loaded two K-blocks ahead
+                const float *xs = nullptr, *wsc = nullptr;
+                float x0 = 0.f, x1 = 0.f, w0 = 0.f, w1 = 0.f;
+                if constexpr (C::kRows) {
+                    if (mrow < p.rows && nc > 0) {
+                        xs = a.xs + (int64_t)p.kb0 * a.R + p.row0 + mrow;
+                        wsc = a.ws +
+                              ((int64_t)p.e * ((a.M + 127) / 128) + (p.col0 + c0) / 128) * p.kb +
+                              p.kb0;
+                        x0 = __ldg(xs);
+                        w0 = __ldg(wsc);
+                        if (p.kb0 + 1 < p.kb1) {
+                            x1 = __ldg(xs + a.R);
+                            w1 = __ldg(wsc + 1);
+                        }
+                    }
+                }
                 const int n_ch = FP8 ? p.kb1 - p.kb0 : (p.kb1 - p.kb0 + kChunk - 1) / kChunk;
                 for (int i = 0; i < n_ch; ++i, ++ch) {
                     const uint32_t buf = ch & 1, sb = ch % kScaleBufs;
                     if (!tc::wait(&s.acc_full[buf], (ch / 2) & 1) ||
-                        (FP8 && !tc::wait(&s.sc_full[sb], (ch / kScaleBufs) & 1))) {
+                        (C::kColScale && !tc::wait(&s.sc_full[sb], (ch / kScaleBufs) & 1))) {
                         if (lane == 0) timeout();
                         ok = false;
                         break;
@@ -649,14 +705,23 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                     tc::fence_after();
                     const uint32_t src = tq + buf * C::BN;
                     const float* sc = scale0 + sb * C::BN + c0;
-                    if (nc == C::kAcc) drain<C, FP8, true>(src, sc, nc, acc);
-                    else if (nc > 0) drain<C, FP8, false>(src, sc, nc, acc);
+                    const float one = x0 * w0;
+                    if constexpr (C::kRows) {
+                        x0 = x1;
+                        w0 = w1;
+                        if (xs && i + 2 < n_ch) {
+                            x1 = __ldg(xs + (int64_t)(i + 2) * a.R);
+                            w1 = __ldg(wsc + i + 2);
+                        }
+                    }
+                    if (nc == C::kAcc) drain<C, FP8, true>(src, sc, one, nc, acc);
+                    else if (nc > 0) drain<C, FP8, false>(src, sc, one, nc, acc);
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) {
                         if (CTAS == 2) tc::arrive_cluster(acc_empty[buf]);
                         else mbar_arrive(&s.acc_empty[buf]);
-                        if (FP8) mbar_arrive(&s.sc_empty[sb]);
+                        if (C::kColScale) mbar_arrive(&s.sc_empty[sb]);
                     }
                 }
             }
@@ -770,6 +835,32 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                         dst[j0 / 8] = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
+            } else if constexpr (C::kRows) {
+                // a thread's columns are consecutive in its row of the output
+                if (mrow < p.rows) {
+                    const int64_t o = (int64_t)(p.row0 + mrow) * a.M + p.col0 + c0;
+#pragma unroll
+                    for (int j0 = 0; j0 < C::kAcc; j0 += 8) {
+                        if (j0 >= nc) break;  // columns come in whole vectors of 8
+                        const float* f = acc + j0;
+                        if (a.out_bf16) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __nv_bfloat162 h =
+                                    __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+                                u[j] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o + j0) =
+                                make_uint4(u[0], u[1], u[2], u[3]);
+                        } else {
+                            float4* dst =
+                                reinterpret_cast<float4*>(static_cast<float*>(a.out) + o + j0);
+                            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+                        }
+                    }
+                }
             } else if (m < a.M) {
                 // a warp writes 32 consecutive values of one row at a time
                 const int64_t o = (int64_t)(p.row0 + c0) * a.M + m;
@@ -849,6 +940,9 @@ coli_status launch_mm(const void* A, const void* B, const MmArgs& a, int N, int 
         ok = encode(&amap, in, A, N, a.R, 0, 64) && encode(&bmap, in, B, K, a.R, 0, 64) &&
              encode(&omap, a.out_bf16 ? kBf16 : kF32, a.out, K, N, a.E, 32);
         big = bmap;  // not used
+    } else if constexpr (C::kRows) {
+        ok = encode(&amap, in, A, K, a.R, 0, kBM) && encode(&bmap, in, B, K, N, a.E, C::kBoxRows);
+        big = omap = bmap;  // not used
     } else {
         ok = encode(&amap, in, A, K, N, a.E, MODE == kFwd ? kBM : 64) &&
              encode(&bmap, in, B, MODE == kFwd ? K : N, a.R, 0, C::kBoxRows) &&
@@ -1000,7 +1094,7 @@ coli_status coli_moe_fp8_grouped_mm(int32_t R, int32_t E, int32_t N, int32_t K, 
     a.ws = w_scale;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return narrow(R, E) ? launch_mm<kFwd, true, 64, 1>(wq, xq, a, N, K, st)
-                        : launch_mm<kFwd, true, 256, 1>(wq, xq, a, N, K, st);
+                        : launch_mm<kFwdRows, true, 256, 1>(xq, wq, a, N, K, st);
 }
 
 }  // extern "C"
