@@ -60,7 +60,10 @@ constexpr int kMaxGrid = 148;
 constexpr int kChunk = 8;              // bf16 K-blocks per accumulator chain
 constexpr int kScaleBufs = 4;
 constexpr int kSmemMax = 227 * 1024;
-constexpr int kMinRange = 4;           // K-blocks of a range of the last wave, at least
+// The last wave is cut into ranges of kMinRange K-blocks at least, and not at
+// all where a whole tile costs a worker at most kCutCost K-blocks more than its
+// range: partial sums take about 5 us to leave and be added up, a K-block 0.4.
+constexpr int kMinRange = 12, kCutCost = 12;
 constexpr int kBand = 8;
 constexpr int kStoreBytes = 32 * 128;  // kDw: staging of one warp's stores
 
@@ -111,6 +114,7 @@ struct Shared {
     uint32_t tmem;
     int abort;
     int last;                              // this CTA finishes the cut tile
+    int kb_max;                            // K-blocks of the longest tile
     int whole, wave, range;                // whole tiles; steps of the last wave, of a range of it
     long long base;                        // first step of the last wave
     long long scan[2][kThreads / 32 + 1];
@@ -186,10 +190,13 @@ struct Walk {
             const int e = group_of(s.tile0, per, full, a.E);
             base = s.step0[e] * per + (full - s.tile0[e] * per) * group_kb(a, e);
         }
-        s.whole = (int)full;
+        const int wave = (int)(steps - base);
+        const int range = max(kMinRange, (wave + workers() - 1) / workers());
+        const bool cut = s.kb_max > range + kCutCost;
+        s.whole = (int)(cut ? full : tiles);
         s.base = base;
-        s.wave = (int)(steps - base);
-        s.range = max(kMinRange, (s.wave + workers() - 1) / workers());
+        s.wave = cut ? wave : 0;
+        s.range = range;
     }
     __device__ __forceinline__ Walk(const MmArgs& a_, const Shared& s_) : a(a_), s(s_) {
         tile = worker();
@@ -317,9 +324,12 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
     constexpr int kStages = stage_count<C>();
     constexpr int CTAS = C::CTAS;
     // Wide tiles hold 128 accumulators and 32 loaded values per epilogue
-    // thread: the epilogue's two warpgroups take registers from the first
-    // (128 x 72 + 256 x 216 = 384 x 168).
+    // thread: the epilogue's two warpgroups take registers from the first (which
+    // needs fewer where it computes no scales): 128 x 72 + 256 x 216 or
+    // 128 x 56 + 256 x 224, both the launch's 384 x 168.
     constexpr bool kSplitRegs = C::kAcc > 64;
+    constexpr int kFrontRegs = C::kRows ? 56 : 72, kEpiRegs = C::kRows ? 224 : 216;
+    static_assert(128 * kFrontRegs + 256 * kEpiRegs <= kThreads * 168, "register split");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage0 = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -345,9 +355,15 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
             mbar_init(&s.sc_empty[i], kEpiWarps);
         }
         s.abort = 0;
+        s.kb_max = MODE == kDw ? 0 : (a.red + C::BK - 1) / C::BK;
         fence_barrier_init();
     }
     if (warp == 2) tc::alloc<CTAS>(&s.tmem, C::kTmemCols);
+    if (warp == 3 && lane == 0) {
+        tc::prefetch_map(&amap);
+        tc::prefetch_map(&bmap);
+    }
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
 
@@ -367,6 +383,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                 } else if (MODE == kDw) {
                     v[i] = 1;
                     w[i] = max(1, (hi - lo + C::BK - 1) / C::BK);
+                    atomicMax(&s.kb_max, (int)w[i]);
                 } else {
                     constexpr int kTileRows = Walk<MODE, C>::kTileRows;
                     v[i] = (hi - lo + kTileRows - 1) / kTileRows;
@@ -424,7 +441,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
     Piece p = {};
 
     if (warp < kEpiWarp0) {
-        if constexpr (kSplitRegs) tc::regs_dec<72>();
+        if constexpr (kSplitRegs) tc::regs_dec<kFrontRegs>();
         if (warp == 0) {
             // ------------------------------ loads --------------------------------
             if (lane == 0) {
@@ -651,7 +668,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
         }
     } else {
         // ------------------------------ epilogue ---------------------------------
-        if constexpr (kSplitRegs) tc::regs_inc<216>();
+        if constexpr (kSplitRegs) tc::regs_inc<kEpiRegs>();
         const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
         const int mrow = q * 32 + lane;       // row of this CTA's part of the tile
         uint8_t* stage_out = store0 + (warp - kEpiWarp0) * kStoreBytes;
@@ -753,16 +770,28 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                 __threadfence();
 #pragma unroll
                 for (int j = 0; j < C::kAcc; ++j) acc[j] = 0.f;
-                for (int c = c_first; c <= c_last; ++c) {
-                    const float* src = part_of(c, c == c_first);
+                // as many loads in flight as registers allow: wide tiles 32 columns
+                // of a part at a time, narrow ones 8 columns of 8 parts (the padding
+                // behind the last column is read too)
+                constexpr int kCols = C::kAcc > 64 ? 32 : 8, kParts = C::kAcc > 64 ? 1 : 8;
+#pragma unroll 1
+                for (int c = c_first; c <= c_last; c += kParts) {
 #pragma unroll
-                    for (int j0 = 0; j0 < C::kAcc; j0 += 16) {
+                    for (int j0 = 0; j0 < C::kAcc; j0 += kCols) {
                         if (j0 >= nc) break;
-                        float f[16];  // all loads of a group in flight (its padding is read too)
+                        float f[kParts][kCols];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) f[j] = __ldcg(src + (j0 + j) * kBM);
+                        for (int i = 0; i < kParts; ++i) {
+                            const float* src = part_of(c + i, c + i == c_first) + j0 * kBM;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[j0 + j] += f[j];
+                            for (int j = 0; j < kCols; ++j)
+                                f[i][j] = kParts == 1 || c + i <= c_last ? __ldcg(src + j * kBM)
+                                                                         : 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                            for (int j = 0; j < kCols; ++j) acc[j0 + j] += f[i][j];
                     }
                 }
             }

@@ -155,6 +155,10 @@ __device__ __forceinline__ void tma_3d(void* dst, const void* map, int c0, int c
             : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // ---- tensor-map stores (parts outside the tensor are not written) ----
 __device__ __forceinline__ void tma_store_3d(const void* map, const void* src, int c0, int c1,
                                              int c2, bool add) {
