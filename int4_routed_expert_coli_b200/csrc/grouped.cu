@@ -14,12 +14,12 @@
 // of kDw) is an MN-major tile, so no transposed copy exists.
 //
 // One CTA per SM, persistent; warp 0 loads (tensor copies, a ring of stages
-// of 128 bytes x rows), warp 1 issues the MMAs, warps 4-11 drain the
+// of 128 bytes x rows), warp 1 issues the MMAs, the last eight warps drain the
 // accumulators.  Tensor memory holds two accumulators; the MMAs of one run
 // while the other is drained:
-//   * a bf16 sum is drained into fp32 registers every kChunk K-blocks: the
-//     tensor cores' fp32 accumulation truncates, and a chain of 6144 products
-//     is 7e-6 off (16384: 2e-5), a chain of 2048 2e-6;
+//   * a bf16 sum is drained into fp32 registers every kChunk K-blocks at most:
+//     the tensor cores' fp32 accumulation truncates, and a chain of 6144
+//     products is 7e-6 off (16384: 2e-5), one of 768 below 1e-6;
 //   * an e4m3 sum is drained every block of 128, times the block's two scales
 //     (the row's and the weight block's, whose product warps 2 and 3 put in
 //     shared memory: a weight tile's 128 rows are one scale block).
@@ -54,11 +54,11 @@ constexpr int kBM = 128;               // M per CTA
 constexpr int kRowBytes = 128;         // bytes of one operand row (or column) per stage
 constexpr int kABytes = kBM * kRowBytes;
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 384;
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kEpiWarps = 8;
 constexpr int kMaxGrid = 148;
-constexpr int kChunk = 8;              // bf16 K-blocks per accumulator chain
+constexpr int kChunk = 12;             // bf16 K-blocks per accumulator chain, at most
 constexpr int kScaleBufs = 4;
+constexpr int kScaleRing = 8;          // kFwdRows: K-blocks whose scales are loaded ahead
 constexpr int kSmemMax = 227 * 1024;
 // The last wave is cut into ranges of kMinRange K-blocks at least, and not at
 // all where a whole tile costs a worker at most kCutCost K-blocks more than its
@@ -99,10 +99,20 @@ struct Cfg {
     static constexpr int kNGrain = 16 * CTAS;              // MMA N in multiples of this
     static constexpr bool kAMn = MODE == kDx || MODE == kDw;
     static constexpr bool kBMn = MODE == kDw;
-    static constexpr int kAcc = BN / 2;                    // accumulators per epilogue thread
     static constexpr bool kColScale = FP8 && !kRows;       // scales per column, in shared memory
-    static constexpr int kScaleBytes = kColScale ? kScaleBufs * BN * 4 : 0;
+    static constexpr int kAcc = BN / 2;                    // accumulators per epilogue thread
+    // Four front warps (loads, MMAs, two that multiply scales or clear), eight of
+    // the epilogue.  A wide tile's epilogue thread holds 128 sums and 32 loaded
+    // values, more than 384 threads can have each (168 registers): the front
+    // warpgroup gives registers to the epilogue's two.
+    static constexpr int kFront = 4;
+    static constexpr bool kSplitRegs = kAcc > 64;
+    static constexpr int kFrontRegs = kRows ? 56 : 72, kEpiRegs = kRows ? 224 : 216;
+    static_assert(128 * kFrontRegs + 256 * kEpiRegs <= 384 * 168, "register split");
+    static constexpr int kThreads = (kFront + kEpiWarps) * 32;
     static constexpr int kStoreStage = MODE == kDw ? kEpiWarps * kStoreBytes : 0;
+    static constexpr int kScaleBytes =
+        kColScale ? kScaleBufs * BN * 4 : kRows && FP8 ? kScaleRing * kEpiWarps * 32 * 8 : 0;
 };
 
 // Everything of shared memory but the stages.
@@ -110,14 +120,16 @@ struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t sc_full[kScaleBufs], sc_empty[kScaleBufs];
-    uint64_t tail_ready[kMaxStages];       // kDw, CTAS = 2: the odd CTA's rows are cleared
+    // kDw, a group's cut last K-block: its copies are done; the rows behind the
+    // group's end are cleared
+    uint64_t tail_full[kMaxStages], tail_ready[kMaxStages];
     uint32_t tmem;
     int abort;
     int last;                              // this CTA finishes the cut tile
     int kb_max;                            // K-blocks of the longest tile
     int whole, wave, range;                // whole tiles; steps of the last wave, of a range of it
     long long base;                        // first step of the last wave
-    long long scan[2][kThreads / 32 + 1];
+    long long scan[2][16];
     int tile0[kMaxExperts + 1];            // first tile (of the first M tile column) of each group
     long long step0[kMaxExperts + 1];      // K-block steps before each group
 };
@@ -263,6 +275,13 @@ struct Walk {
     }
 };
 
+// Accumulator chains of n K-blocks: as few as possible, of equal lengths (a
+// short one behind a long one would leave the drain no time).
+template <bool FP8>
+__device__ __forceinline__ int chains(int n) { return FP8 ? n : (n + kChunk - 1) / kChunk; }
+template <bool FP8>
+__device__ __forceinline__ int chain_len(int n) { return (n + chains<FP8>(n) - 1) / chains<FP8>(n); }
+
 // Columns of the MMA: the valid ones rounded up to its grain.
 template <class C>
 __device__ __forceinline__ int mma_n(int n) {
@@ -270,12 +289,12 @@ __device__ __forceinline__ int mma_n(int n) {
 }
 
 // Add one accumulator's columns (times their scales: `sc` per column or `one`
-// for all) to a thread's sums.  The
-// loads of 16 columns run under the sums of the 16 before; a whole tile's loop
-// has no branches, so its instructions interleave.
-template <class C, bool FP8, bool WHOLE>
+// for all) to a thread's sums, and call `release` once they are all loaded.
+// The loads of 16 columns run under the sums of the 16 before; a whole tile's
+// loop has no branches, so its instructions interleave.
+template <class C, bool FP8, bool WHOLE, class Release>
 __device__ __forceinline__ void drain(uint32_t src, const float* sc, float one, int nc,
-                                      float (&acc)[C::kAcc]) {
+                                      float (&acc)[C::kAcc], Release release) {
     constexpr int kGroups = C::kAcc / 16;
     uint32_t v[2][16];
     tc::ld16(src, v[0]);
@@ -291,14 +310,14 @@ __device__ __forceinline__ void drain(uint32_t src, const float* sc, float one, 
         tc::ld_wait(w);
         if (g + 1 < kGroups && (WHOLE || (g + 1) * 16 < nc))
             tc::ld16(src + (g + 1) * 16, v[(g + 1) & 1]);
+        else
+            release();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float* d = acc + g * 16 + 4 * j;
             if constexpr (C::kRows) {
-                d[0] += __uint_as_float(w[4 * j]) * one;
-                d[1] += __uint_as_float(w[4 * j + 1]) * one;
-                d[2] += __uint_as_float(w[4 * j + 2]) * one;
-                d[3] += __uint_as_float(w[4 * j + 3]) * one;
+                tc::fma2(d, w + 4 * j, one);
+                tc::fma2(d + 2, w + 4 * j + 2, one);
             } else if constexpr (C::kColScale) {
                 d[0] += __uint_as_float(w[4 * j]) * f[j].x;
                 d[1] += __uint_as_float(w[4 * j + 1]) * f[j].y;
@@ -315,7 +334,7 @@ __device__ __forceinline__ void drain(uint32_t src, const float* sc, float one, 
 }
 
 template <int MODE, bool FP8, int BN_, int CTAS_>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<MODE, FP8, BN_, CTAS_>::kThreads, 1)
 grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                   const __grid_constant__ CUtensorMap bmap,
                   const __grid_constant__ CUtensorMap bmap_big,
@@ -323,13 +342,6 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
     using C = Cfg<MODE, FP8, BN_, CTAS_>;
     constexpr int kStages = stage_count<C>();
     constexpr int CTAS = C::CTAS;
-    // Wide tiles hold 128 accumulators and 32 loaded values per epilogue
-    // thread: the epilogue's two warpgroups take registers from the first (which
-    // needs fewer where it computes no scales): 128 x 72 + 256 x 216 or
-    // 128 x 56 + 256 x 224, both the launch's 384 x 168.
-    constexpr bool kSplitRegs = C::kAcc > 64;
-    constexpr int kFrontRegs = C::kRows ? 56 : 72, kEpiRegs = C::kRows ? 224 : 216;
-    static_assert(128 * kFrontRegs + 256 * kEpiRegs <= kThreads * 168, "register split");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stage0 = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -344,7 +356,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
-            mbar_init(&s.tail_ready[i], 1);
+            mbar_init(&s.tail_full[i], 1);
+            mbar_init(&s.tail_ready[i], CTAS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.acc_full[i], 1);
@@ -358,8 +371,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
         s.kb_max = MODE == kDw ? 0 : (a.red + C::BK - 1) / C::BK;
         fence_barrier_init();
     }
-    if (warp == 2) tc::alloc<CTAS>(&s.tmem, C::kTmemCols);
-    if (warp == 3 && lane == 0) {
+    if (warp == 1) tc::alloc<CTAS>(&s.tmem, C::kTmemCols);
+    if (threadIdx.x == 0) {
         tc::prefetch_map(&amap);
         tc::prefetch_map(&bmap);
     }
@@ -368,13 +381,14 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
     pdl_wait();
 
     // Tiles and K-block steps before each group (of one M tile): a scan over
-    // the groups, three per thread.  An impossible offset pair is reported and
+    // the groups, kPer per thread.  An impossible offset pair is reported and
     // gets no tile.
     {
-        long long v[3], w[3], sum_v = 0, sum_w = 0;
+        constexpr int kPer = (kMaxExperts + 1 + C::kThreads - 1) / C::kThreads;
+        long long v[kPer], w[kPer], sum_v = 0, sum_w = 0;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int e = threadIdx.x * 3 + i;
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
             v[i] = w[i] = 0;
             if (e < a.E) {
                 const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
@@ -414,8 +428,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
             bw += s.scan[1][i];
         }
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int e = threadIdx.x * 3 + i;
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
             if (e <= a.E) {
                 s.tile0[e] = (int)bv;
                 s.step0[e] = bw;
@@ -440,13 +454,13 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
     Walk<MODE, C> walk(a, s);
     Piece p = {};
 
-    if (warp < kEpiWarp0) {
-        if constexpr (kSplitRegs) tc::regs_dec<kFrontRegs>();
+    if (warp < C::kFront) {
+        if constexpr (C::kSplitRegs) tc::regs_dec<C::kFrontRegs>();
         if (warp == 0) {
             // ------------------------------ loads --------------------------------
             if (lane == 0) {
                 uint32_t it = 0;
-                uint32_t tails = 0;   // odd CTA: parity of the next use of each stage's own barrier
+                uint32_t tails = 0;   // parity of the next use of each stage's tail barrier
                 int last_tail = -1;
                 // boxes and bytes of one K-block of CTA `r` of the pair
                 auto boxes_of = [&](int r) {
@@ -475,24 +489,21 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                         uint8_t* sa = stage_ptr(i);
                         uint8_t* sb = sa + kABytes;
                         // copies complete on the barrier of the CTA that issues the
-                        // MMAs; a group's cut last K-block on each CTA's own, since
-                        // each clears rows of it first (the odd CTA's `full` barriers
-                        // have no other use)
-                        const bool tail = MODE == kDw && CTAS == 2 && p.rows - kb * C::BK < C::BK;
+                        // MMAs; those of a group's cut last K-block on each CTA's own
+                        // tail barrier, for the warp that clears rows of it
+                        const bool tail = MODE == kDw && p.rows - kb * C::BK < C::BK;
                         uint32_t bar;
-                        if (CTAS == 1) {
-                            mbar_arrive_expect_tx(&s.full[i], bytes);
-                            bar = smem_addr(&s.full[i]);
-                        } else if (rank == 0) {
-                            mbar_arrive_expect_tx(&s.full[i], tail ? bytes : all);
-                            bar = tc::cluster_addr(&s.full[i], 0);
-                        } else if (tail) {
-                            mbar_arrive_expect_tx(&s.full[i], bytes);
-                            bar = tc::cluster_addr(&s.full[i], 1);
+                        if (tail) {
+                            if (rank == 0) mbar_arrive(&s.full[i]);
+                            mbar_arrive_expect_tx(&s.tail_full[i], bytes);
+                            bar = CTAS == 2 ? tc::cluster_addr(&s.tail_full[i], rank)
+                                            : smem_addr(&s.tail_full[i]);
                             tails ^= 1u << i;
                             last_tail = i;
                         } else {
-                            bar = tc::cluster_addr(&s.full[i], 0);
+                            if (rank == 0) mbar_arrive_expect_tx(&s.full[i], all);
+                            bar = CTAS == 2 ? tc::cluster_addr(&s.full[i], 0)
+                                            : smem_addr(&s.full[i]);
                         }
                         if constexpr (MODE == kFwd) {
                             tc::tma_3d<CTAS>(sa, &amap, kb * C::BK, p.m0, p.e, bar);
@@ -536,8 +547,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                     if (rank == 0)
                         for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
                             tc::wait(&s.full[j % kStages], (j / kStages) & 1);
-                    else if (last_tail >= 0)
-                        tc::wait(&s.full[last_tail], (tails >> last_tail & 1) ^ 1);
+                    if (last_tail >= 0)
+                        tc::wait(&s.tail_full[last_tail], (tails >> last_tail & 1) ^ 1);
                 }
             }
         } else if (warp == 1) {
@@ -548,31 +559,25 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                 C::kAMn ? tc::desc_base(64 * kRowBytes, 1024) : tc::desc_base(0, 1024);
             const uint64_t bbase =
                 C::kBMn ? tc::desc_base(64 * kRowBytes, 1024) : tc::desc_base(0, 1024);
-            // Clear the rows behind a group's end in this CTA's part of a stage
-            // (both operands: they may hold infinities), up to the next MMA step.
-            auto clear_tail = [&](int i, int valid) {
-                const int half = mma_n<C>(p.n) / CTAS;
-                const int n = max(0, min(half, p.n - (int)rank * half));
-                const int boxes = 2 + (n + 63) / 64;
-                const int chunks = ((valid + 15) / 16 * 16 - valid) * 8;
-                for (int b = 0; b < boxes; ++b)
-                    for (int j = lane; j < chunks; j += 32)
-                        *reinterpret_cast<uint4*>(stage_ptr(i) + b * 64 * kRowBytes +
-                                                  valid * kRowBytes + j * 16) =
-                            make_uint4(0, 0, 0, 0);
-                fence_proxy_async();
-                __syncwarp();
-            };
             uint32_t it = 0, ch = 0;
             uint32_t tails = 0;  // parity of each stage's next cut last K-block
             if (rank == 0) {
-                while (!*abort && walk.next(p)) {
-                    if (MODE == kDw && p.rows == 0) continue;
+                Piece nxt = {};
+                bool more = walk.next(nxt);
+                while (!*abort && more) {
+                    p = nxt;
+                    bool looked = false;  // the next piece is looked up under this one's MMAs
+                    if (MODE == kDw && p.rows == 0) {
+                        more = walk.next(nxt);
+                        continue;
+                    }
                     const uint32_t id =
                         tc::idesc(kBM * CTAS, mma_n<C>(p.n), FP8 ? 0 : 1, C::kAMn, C::kBMn);
                     bool ok = true;
+                    const int len = chain_len<FP8>(p.kb1 - p.kb0);
+                    int in_chain = 0;
                     for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
-                        const bool first = FP8 || (kb - p.kb0) % kChunk == 0;
+                        const bool first = in_chain == 0;
                         const uint32_t buf = ch & 1;
                         if (first && ch >= 2) ok = tc::wait(&s.acc_empty[buf], (ch / 2 - 1) & 1);
                         const int i = it % kStages;
@@ -585,10 +590,10 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                         if constexpr (MODE == kDw) {
                             const int valid = p.rows - kb * C::BK;
                             if (valid < C::BK) {
+                                // a group's cut last K-block: whole MMA steps behind its
+                                // end are left out, warp 2 clears the rest of the last
                                 steps = (valid + 15) / 16;
-                                clear_tail(i, valid);
-                                if (CTAS == 2 &&
-                                    !tc::wait_cluster(&s.tail_ready[i], tails >> i & 1)) {
+                                if (!tc::wait_cluster(&s.tail_ready[i], tails >> i & 1)) {
                                     timeout();
                                     ok = false;
                                     break;
@@ -597,8 +602,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                             }
                         }
                         tc::fence_after();
-                        const bool last =
-                            FP8 || kb + 1 == p.kb1 || (kb - p.kb0) % kChunk == kChunk - 1;
+                        const bool last = kb + 1 == p.kb1 || in_chain + 1 == len;
+                        in_chain = last ? 0 : in_chain + 1;
                         if (lane == 0) {
                             const uint32_t sa = smem_addr(stage_ptr(i));
                             const uint64_t ad = tc::desc_at(abase, sa);
@@ -614,24 +619,45 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                         }
                         __syncwarp();
                         if (last) ++ch;
+                        if (!looked) {
+                            more = walk.next(nxt);
+                            looked = true;
+                        }
                     }
                     if (!ok) break;
                 }
-            } else if (MODE == kDw) {
-                // the odd CTA of a pair only clears its part of cut last K-blocks
-                while (!*abort && walk.next(p)) {
-                    if (p.rows == 0) continue;
-                    it += p.kb1 - p.kb0;
-                    const int valid = p.rows - (p.kb1 - 1) * C::BK;
-                    if (valid >= C::BK) continue;
-                    const int i = (it - 1) % kStages;
-                    if (!tc::wait(&s.full[i], tails >> i & 1)) {
-                        timeout();
-                        break;
-                    }
-                    tails ^= 1u << i;
-                    clear_tail(i, valid);
-                    if (lane == 0) tc::arrive_release_cluster(tc::cluster_addr(&s.tail_ready[i], 0));
+            }
+        } else if (MODE == kDw && warp == 2) {
+            // ------ kDw: clear what lies behind a group's end in its last K-block ------
+            // (rows of the next group, in both operands: they may hold infinities), up
+            // to the next MMA step.  In a pair each CTA clears its own part.
+            uint32_t it = 0, tails = 0;
+            while (!*abort && walk.next(p)) {
+                if (p.rows == 0) continue;
+                it += p.kb1 - p.kb0;
+                const int valid = p.rows - (p.kb1 - 1) * C::BK;
+                if (valid >= C::BK) continue;
+                const int i = (it - 1) % kStages;
+                if (!tc::wait(&s.tail_full[i], tails >> i & 1)) {
+                    timeout();
+                    break;
+                }
+                tails ^= 1u << i;
+                const int half = mma_n<C>(p.n) / CTAS;
+                const int n = max(0, min(half, p.n - (int)rank * half));
+                const int boxes = 2 + (n + 63) / 64;
+                const int chunks = ((valid + 15) / 16 * 16 - valid) * 8;
+                for (int b = 0; b < boxes; ++b)
+                    for (int j = lane; j < chunks; j += 32)
+                        *reinterpret_cast<uint4*>(stage_ptr(i) + b * 64 * kRowBytes +
+                                                  valid * kRowBytes + j * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CTAS == 2)
+                        tc::arrive_release_cluster(tc::cluster_addr(&s.tail_ready[i], 0));
+                    else mbar_arrive(&s.tail_ready[i]);
                 }
             }
         } else if constexpr (C::kColScale) {
@@ -668,10 +694,10 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
         }
     } else {
         // ------------------------------ epilogue ---------------------------------
-        if constexpr (kSplitRegs) tc::regs_inc<kEpiRegs>();
-        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        if constexpr (C::kSplitRegs) tc::regs_inc<C::kEpiRegs>();
+        const int q = warp & 3, half = (warp - C::kFront) >> 2;
         const int mrow = q * 32 + lane;       // row of this CTA's part of the tile
-        uint8_t* stage_out = store0 + (warp - kEpiWarp0) * kStoreBytes;
+        uint8_t* stage_out = store0 + (warp - C::kFront) * kStoreBytes;
         const uint32_t acc_empty[2] = {
             CTAS == 2 ? tc::cluster_addr(&s.acc_empty[0], 0) : smem_addr(&s.acc_empty[0]),
             CTAS == 2 ? tc::cluster_addr(&s.acc_empty[1], 0) : smem_addr(&s.acc_empty[1])};
@@ -693,24 +719,29 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                 if (a.accumulate) continue;  // nothing to add
             } else {
                 // kFwdRows: this thread's row has one scale per K-block, its columns
-                // one weight scale; both are loaded two K-blocks ahead
+                // one weight scale.  Each thread copies its own two numbers into its
+                // own ring in shared memory, kScaleRing - 1 K-blocks ahead.
                 const float *xs = nullptr, *wsc = nullptr;
-                float x0 = 0.f, x1 = 0.f, w0 = 0.f, w1 = 0.f;
+                float2* ring = reinterpret_cast<float2*>(scale0) + (threadIdx.x - C::kFront * 32);
+                auto fetch = [&](int i) {
+                    if (xs && i < p.kb1 - p.kb0) {
+                        float2* slot = ring + (i & (kScaleRing - 1)) * (kEpiWarps * 32);
+                        cp_async4(&slot->x, xs + (int64_t)i * a.R);
+                        cp_async4(&slot->y, wsc + i);
+                    }
+                    cp_async_commit();
+                };
                 if constexpr (C::kRows) {
                     if (mrow < p.rows && nc > 0) {
                         xs = a.xs + (int64_t)p.kb0 * a.R + p.row0 + mrow;
                         wsc = a.ws +
                               ((int64_t)p.e * ((a.M + 127) / 128) + (p.col0 + c0) / 128) * p.kb +
                               p.kb0;
-                        x0 = __ldg(xs);
-                        w0 = __ldg(wsc);
-                        if (p.kb0 + 1 < p.kb1) {
-                            x1 = __ldg(xs + a.R);
-                            w1 = __ldg(wsc + 1);
-                        }
                     }
+                    for (int i = 0; i < kScaleRing - 1; ++i) fetch(i);
                 }
-                const int n_ch = FP8 ? p.kb1 - p.kb0 : (p.kb1 - p.kb0 + kChunk - 1) / kChunk;
+                const int len = chain_len<FP8>(p.kb1 - p.kb0);
+                const int n_ch = (p.kb1 - p.kb0 + len - 1) / len;
                 for (int i = 0; i < n_ch; ++i, ++ch) {
                     const uint32_t buf = ch & 1, sb = ch % kScaleBufs;
                     if (!tc::wait(&s.acc_full[buf], (ch / 2) & 1) ||
@@ -722,24 +753,25 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                     tc::fence_after();
                     const uint32_t src = tq + buf * C::BN;
                     const float* sc = scale0 + sb * C::BN + c0;
-                    const float one = x0 * w0;
+                    float one = 0.f;
                     if constexpr (C::kRows) {
-                        x0 = x1;
-                        w0 = w1;
-                        if (xs && i + 2 < n_ch) {
-                            x1 = __ldg(xs + (int64_t)(i + 2) * a.R);
-                            w1 = __ldg(wsc + i + 2);
+                        tc::cp_async_wait<kScaleRing - 2>();
+                        const float2 f = ring[(i & (kScaleRing - 1)) * (kEpiWarps * 32)];
+                        one = f.x * f.y;
+                        fetch(i + kScaleRing - 1);
+                    }
+                    auto release = [&]() {
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (CTAS == 2) tc::arrive_cluster(acc_empty[buf]);
+                            else mbar_arrive(&s.acc_empty[buf]);
+                            if (C::kColScale) mbar_arrive(&s.sc_empty[sb]);
                         }
-                    }
-                    if (nc == C::kAcc) drain<C, FP8, true>(src, sc, one, nc, acc);
-                    else if (nc > 0) drain<C, FP8, false>(src, sc, one, nc, acc);
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (CTAS == 2) tc::arrive_cluster(acc_empty[buf]);
-                        else mbar_arrive(&s.acc_empty[buf]);
-                        if (C::kColScale) mbar_arrive(&s.sc_empty[sb]);
-                    }
+                    };
+                    if (nc == C::kAcc) drain<C, FP8, true>(src, sc, one, nc, acc, release);
+                    else if (nc > 0) drain<C, FP8, false>(src, sc, one, nc, acc, release);
+                    else release();
                 }
             }
             if (!ok) break;
@@ -760,7 +792,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                     if (j < nc) __stcg(mine + j * kBM, acc[j]);
                 __threadfence();
                 named_barrier(1, kEpiWarps * 32);
-                if (warp == kEpiWarp0 && lane == 0) {
+                if (warp == C::kFront && lane == 0) {
                     int* count = a.counters + c_first * CTAS + rank;
                     s.last = atomicAdd(count, 1) == c_last - c_first;
                     if (s.last) *count = 0;
@@ -916,7 +948,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
     // a pair ends together: the even CTA's MMAs read the odd one's memory, the
     // odd one's epilogue arrives on the even one's barriers
     if constexpr (CTAS == 2) tc::cluster_sync();
-    if (warp == 2) {
+    if (warp == 1) {
         tc::fence_after();
         tc::dealloc<CTAS>(tmem, C::kTmemCols);
     }
@@ -992,7 +1024,7 @@ coli_status launch_mm(const void* A, const void* B, const MmArgs& a, int N, int 
     const int grid = std::max(CTAS, std::min(sms, kMaxGrid) / CTAS * CTAS);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];

@@ -245,6 +245,22 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// d[0..1] += v[0..1] * s as one packed instruction (half the issue slots, which
+// the warps that feed the tensor cores share).
+__device__ __forceinline__ void fma2(float* d, const uint32_t* v, float s) {
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\t"
+        "fma.rn.f32x2 a, b, c, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(d[0]), "+f"(d[1])
+        : "f"(__uint_as_float(v[0])), "f"(__uint_as_float(v[1])), "f"(s));
+}
+
+// Wait until at most N of this thread's latest cp.async groups are in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---- register split between warpgroups ----
 template <int N>
 __device__ __forceinline__ void regs_dec() {
@@ -254,5 +270,6 @@ template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
+
 }  // namespace tc
 }  // namespace coli
