@@ -9,13 +9,15 @@
 // fp32; s and o are each rounded once, at their store, and o is computed from
 // the unrounded s.
 //
-// Backward, from the stored s and y (a = do pre_w, r and ry the two inverse
-// RMS values, recomputed: a row is in hand anyway, so nothing is saved for it):
-//   ds' = ds + r (a - s r^2 mean(a s))      dx = ds'
+// Backward, from the stored s and y (r and ry: the two inverse RMS values,
+// recomputed, a row is in hand anyway; A = alpha times a token's gate, cp = post_w
+// times a channel's gate):
+//   d  = ds + r do pre_w - r^3 mean(do pre_w s) s        dx = d
+//   dy = ry A cp d - ry^3 mean(A cp d y) y               (no post_w: dy = A cp d)
 //   dpre_w = sum_t do s r
-//   dgate = alpha sum (ds' n) over the tokens (channel) or channels (token)
-//   dn = alpha g ds',  b = dn post_w
-//   dpost_w = sum_t dn y ry,  dy = ry (b - y ry^2 mean(b y))   (no post_w: dy = dn)
+//   C = sum_t gate_token d y ry:  dpost_w = alpha gate_channel C,
+//   a channel gate's dgate = alpha post_w C, a token's = alpha ry sum_h cp d y
+// so a row needs four sums (s^2, do pre_w s, y^2, cp d y) and a column two.
 //
 // Both directions move each value once and are bound by memory traffic.
 #include <algorithm>
@@ -41,7 +43,7 @@ struct NormArgs {
     const void *go, *gs, *s;  // gradients of o and s (nullable), the stored s
     void *dx, *dy;
     float *dpre_w, *dpost_w, *dgate;
-    float* part;              // [grid][3][H] column partials: pre_w, post_w, gate
+    float* part;              // [grid][2][H] column partials: dpre_w, C
 };
 
 // VEC consecutive values starting at element i (16-byte aligned for VEC = 8).
@@ -204,16 +206,17 @@ block_norm_bwd_kernel(const NormArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int H = a.H;
-    float c_pre[NCH][VEC], c_post[NCH][VEC], c_gate[NCH][VEC];
+    const float inv_h = 1.f / (float)H;
+    float c_pre[NCH][VEC], c_y[NCH][VEC];
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) c_pre[c][j] = c_post[c][j] = c_gate[c][j] = 0.f;
+        for (int j = 0; j < VEC; ++j) c_pre[c][j] = c_y[c][j] = 0.f;
 
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = (int64_t)t * H;
         float s[NCH][VEC], y[NCH][VEC], g[NCH][VEC], d[NCH][VEC];
-        float q[3] = {0.f, 0.f, 0.f};  // sum s^2, sum a s, sum y^2
+        float q[3] = {0.f, 0.f, 0.f};  // sum s^2, sum do pre_w s, sum y^2
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int h = (c * blockDim.x + threadIdx.x) * VEC;
@@ -249,12 +252,12 @@ block_norm_bwd_kernel(const NormArgs a) {
                 for (int j = 0; j < VEC; ++j) q[2] += y[c][j] * y[c][j];
         }
         block_sums<3>(q, tmp[0]);
-        const float inv_h = 1.f / (float)H;
-        const float r = rsqrtf(q[0] / (float)H + a.eps);
-        const float ry = a.post_w ? rsqrtf(q[2] / (float)H + a.eps) : 1.f;
-        const float k1 = r * r * (q[1] * inv_h);
+        const float r = rsqrtf(q[0] * inv_h + a.eps);
+        const float ry = a.post_w ? rsqrtf(q[2] * inv_h + a.eps) : 1.f;
+        const float rk = r * (r * r * (q[1] * inv_h));
         const float gt = a.gate_kind == COLI_GATE_TOKEN ? a.gate[t] : 1.f;
-        float p[2] = {0.f, 0.f};  // sum b y, sum ds' n
+        const float A = a.alpha * gt, cy = gt * ry;
+        float p[1] = {0.f};  // sum cp d y
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int h = (c * blockDim.x + threadIdx.x) * VEC;
@@ -264,27 +267,25 @@ block_norm_bwd_kernel(const NormArgs a) {
                 load_vals<VEC>(a.pre_w, h, 0, w);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    c_pre[c][j] += g[c][j] * (s[c][j] * r);
-                    d[c][j] += r * (g[c][j] * w[j] - s[c][j] * k1);
+                    c_pre[c][j] += (g[c][j] * s[c][j]) * r;
+                    d[c][j] += r * (g[c][j] * w[j]) - rk * s[c][j];
                 }
             }
             if (a.dx) store_vals<VEC>(a.dx, row + h, a.x_bf16, d[c]);
             if (a.y) {
-                float pw[VEC], cg[VEC];
+                float cp[VEC];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) pw[j] = cg[j] = 1.f;
-                if (a.post_w) load_vals<VEC>(a.post_w, h, 0, pw);
-                if (a.gate_kind == COLI_GATE_CHANNEL) load_vals<VEC>(a.gate, h, 0, cg);
+                for (int j = 0; j < VEC; ++j) cp[j] = 1.f;
+                if (a.post_w) load_vals<VEC>(a.post_w, h, 0, cp);
+                if (a.gate_kind == COLI_GATE_CHANNEL) {
+                    load_vals<VEC>(a.gate, h, 0, w);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) cp[j] *= w[j];
+                }
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    const float yh = y[c][j] * ry;       // normalised block output
-                    const float ds = a.alpha * d[c][j];
-                    const float dg = ds * (yh * pw[j]);
-                    p[1] += dg;
-                    c_gate[c][j] += dg;
-                    const float dn = ds * (gt * cg[j]);
-                    c_post[c][j] += dn * yh;
-                    d[c][j] = dn * pw[j];                // b
+                    c_y[c][j] += (d[c][j] * y[c][j]) * cy;
+                    d[c][j] *= cp[j];
                     p[0] += d[c][j] * y[c][j];
                 }
             }
@@ -293,55 +294,438 @@ block_norm_bwd_kernel(const NormArgs a) {
             __syncthreads();  // tmp[0] is read by all before the next row writes it
             continue;
         }
-        block_sums<2>(p, tmp[1]);
-        const float k2 = a.post_w ? ry * ry * (p[0] * inv_h) : 0.f;
+        block_sums<1>(p, tmp[1]);
+        const float c1 = ry * A, c2 = a.post_w ? ry * (ry * ry * (A * p[0] * inv_h)) : 0.f;
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int h = (c * blockDim.x + threadIdx.x) * VEC;
             if (h >= H || !a.dy) continue;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) d[c][j] = ry * (d[c][j] - y[c][j] * k2);
+            for (int j = 0; j < VEC; ++j) d[c][j] = c1 * d[c][j] - c2 * y[c][j];
             store_vals<VEC>(a.dy, row + h, a.y_bf16, d[c]);
         }
-        if (a.dgate && a.gate_kind == COLI_GATE_TOKEN && threadIdx.x == 0) a.dgate[t] = p[1];
+        if (a.dgate && a.gate_kind == COLI_GATE_TOKEN && threadIdx.x == 0)
+            a.dgate[t] = a.alpha * ry * p[0];
     }
-    float* part = a.part + (int64_t)blockIdx.x * 3 * H;
+    if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
         const int h = (c * blockDim.x + threadIdx.x) * VEC;
         if (h >= H) continue;
         if (a.dpre_w) store_vals<VEC>(part, h, 0, c_pre[c]);
-        if (a.dpost_w) store_vals<VEC>(part + H, h, 0, c_post[c]);
-        if (a.dgate && a.gate_kind == COLI_GATE_CHANNEL) store_vals<VEC>(part + 2 * H, h, 0, c_gate[c]);
+        if (a.y) store_vals<VEC>(part + H, h, 0, c_y[c]);
     }
 }
 
-// Column sums: out[h] = sum over the CTAs of part[cta][which][h], 32 columns
-// per block, 8 warps over the CTAs; fixed order (each warp its strided share
-// ascending, then the warps ascending).
+// ---- many rows of whole 16-byte vectors ------------------------------------------
+// A CTA walks rows blockIdx.x, + gridDim.x, ... .  Each thread owns VPT vectors
+// of 8 columns and copies them (cp.async) into its own places of a ring in
+// shared memory, rows ahead of the one it works on, so that the memory system
+// has rows in flight whatever the row reductions wait for; nobody else reads
+// those places, so the copies need no barrier.  The weights lie in shared
+// memory too: read from L2 for every row they would be more bytes than the row
+// itself.  The types are template parameters and the loops have no branches
+// (a vector past the row's end has places of its own that nothing fills;
+// its sums are masked and its stores left out), so that a row's loads and sums interleave.
+constexpr int kVpt = 2;                 // vectors per thread
+constexpr int kRingMaxThreads = 512;
+
+// Pairs of fp32 values in one 64-bit register: one instruction for both.  (Issue
+// slots bound the scalar form: 52 and 91 us at 4096 x 6144 bf16.)
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    const float2 f = unpair(v);
+    return f.x + f.y;
+}
+
+// 8 values as four pairs.
+template <bool BF16>
+__device__ __forceinline__ void load_pairs(const char* p, f2 (&v)[4]) {
+    if constexpr (BF16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = pair(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+    } else {
+        const ulonglong2 x = reinterpret_cast<const ulonglong2*>(p)[0];
+        const ulonglong2 z = reinterpret_cast<const ulonglong2*>(p)[1];
+        v[0] = x.x; v[1] = x.y; v[2] = z.x; v[3] = z.y;
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ void store_pairs(void* p, int64_t i, const f2 (&v)[4]) {
+    if constexpr (BF16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = unpair(v[j]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        ulonglong2* q = reinterpret_cast<ulonglong2*>(static_cast<float*>(p) + i);
+        q[0] = make_ulonglong2(v[0], v[1]);
+        q[1] = make_ulonglong2(v[2], v[3]);
+    }
+}
+
+struct RingPlan {
+    int slots;            // rows in the ring
+    const void* src[4];   // copied arrays (null: absent)
+    uint32_t at[4];       // byte offset of each in a slot
+    uint32_t slot;        // bytes of a slot
+    uint32_t weights;     // bytes of the weights before the ring
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+}
+// At most `n` of this thread's latest groups in flight (n < 7).
+__device__ __forceinline__ void cp_async_wait_n(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    }
+}
+
+// One thread's view of the ring.
+struct RowRing {
+    const RingPlan& p;
+    char* base;
+    int H, T;
+
+    // column of vector c, and whether the row has it
+    static __device__ __forceinline__ int col(int c) {
+        return (c * blockDim.x + threadIdx.x) * 8;
+    }
+    __device__ __forceinline__ bool live(int c) const { return col(c) < H; }
+    // the same, clamped to the row (weights)
+    __device__ __forceinline__ int wcol(int c) const { return min(col(c), H - 8); }
+
+    template <bool BF16>
+    __device__ __forceinline__ void copy(int k, int64_t t, char* slot) const {
+        constexpr int kSize = BF16 ? 2 : 4;
+        if (!p.src[k]) return;
+        const char* g = static_cast<const char*>(p.src[k]) + t * H * kSize;
+#pragma unroll
+        for (int c = 0; c < kVpt; ++c) {
+            if (!live(c)) continue;
+            cp_async16(slot + p.at[k] + col(c) * kSize, g + col(c) * kSize);
+            if (!BF16) cp_async16(slot + p.at[k] + col(c) * kSize + 16, g + col(c) * kSize + 16);
+        }
+    }
+    // This thread's copies of row t into slot i, one group (empty past the end).
+    template <bool B0, bool B1, bool B2, bool B3>
+    __device__ __forceinline__ void fetch(int64_t t, int i) const {
+        if (t < T) {
+            char* slot = base + (size_t)i * p.slot;
+            copy<B0>(0, t, slot);
+            copy<B1>(1, t, slot);
+            copy<B2>(2, t, slot);
+            copy<B3>(3, t, slot);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    template <bool BF16>
+    __device__ __forceinline__ void load(int k, int i, int c, f2 (&v)[4]) const {
+        load_pairs<BF16>(base + (size_t)i * p.slot + p.at[k] + col(c) * (BF16 ? 2 : 4), v);
+    }
+};
+
+// The weights into shared memory: pre_w, and post_w times a channel's gate
+// (ones where there is none), each [2][H / 2]: a vector's first four values in
+// the first plane, the others in the second (a warp's 16-byte reads then fall
+// on consecutive addresses).
+__device__ __forceinline__ void stage_weights(float* w_pre, float* w_cp, const NormArgs& a) {
+    const int H = a.H;
+    for (int h = threadIdx.x * 4; h < H; h += blockDim.x * 4) {
+        float4 v = make_float4(1.f, 1.f, 1.f, 1.f);
+        const int at = (h & 4 ? H / 2 : 0) + h / 8 * 4;
+        if (a.pre_w) v = __ldg(reinterpret_cast<const float4*>(a.pre_w + h));
+        *reinterpret_cast<float4*>(w_pre + at) = v;
+        v = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (a.post_w) v = __ldg(reinterpret_cast<const float4*>(a.post_w + h));
+        if (a.gate_kind == COLI_GATE_CHANNEL) {
+            const float4 g = __ldg(reinterpret_cast<const float4*>(a.gate + h));
+            v.x *= g.x; v.y *= g.y; v.z *= g.z; v.w *= g.w;
+        }
+        *reinterpret_cast<float4*>(w_cp + at) = v;
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void load_weights(const float* w, int H, int col, f2 (&v)[4]) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(w + col / 2);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(w + H / 2 + col / 2);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+
+template <bool XB, bool YB, bool OB>
+__global__ void __launch_bounds__(kRingMaxThreads)
+block_norm_ring_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RingPlan p) {
+    extern __shared__ __align__(128) char smem[];
+    __shared__ float tmp[2][32];
+    const int H = a.H;
+    float* w_pre = reinterpret_cast<float*>(smem);
+    float* w_cp = w_pre + H;
+    const RowRing ring{p, smem + p.weights, H, a.T};
+    const float inv_h = 1.f / (float)H;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = 0; i < p.slots - 1; ++i)
+        ring.fetch<XB, YB, false, false>(blockIdx.x + (int64_t)i * gridDim.x, i);
+    stage_weights(w_pre, w_cp, a);
+    int slot = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        cp_async_wait_n(p.slots - 2);
+        const int64_t row = t * H;
+        f2 s[kVpt][4], y[kVpt][4];
+        float q[1] = {0.f};
+#pragma unroll
+        for (int c = 0; c < kVpt; ++c) {
+            ring.load<XB>(0, slot, c, s[c]);
+            if (a.y) ring.load<YB>(1, slot, c, y[c]);
+            if (a.post_w) {
+                f2 z = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z = fma2(y[c][j], y[c][j], z);
+                q[0] += ring.live(c) ? sum2(z) : 0.f;
+            }
+        }
+        {   // the slot is in registers: fetch the row that takes the place before it
+            const int next = slot == 0 ? p.slots - 1 : slot - 1;
+            ring.fetch<XB, YB, false, false>(t + (int64_t)(p.slots - 1) * gridDim.x, next);
+            slot = slot + 1 == p.slots ? 0 : slot + 1;
+        }
+        if (a.y) {
+            float A = a.alpha;
+            if (a.gate_kind == COLI_GATE_TOKEN) A *= __ldg(a.gate + t);
+            if (a.post_w) {
+                block_sums<1>(q, tmp[0]);
+                A *= rsqrtf(q[0] * inv_h + a.eps);
+            }
+            const f2 A2 = pair(A, A);
+#pragma unroll
+            for (int c = 0; c < kVpt; ++c) {
+                f2 w[4];
+                load_weights(w_cp, H, ring.wcol(c), w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[c][j] = fma2(A2, mul2(y[c][j], w[j]), s[c][j]);
+            }
+        }
+        q[0] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kVpt; ++c) {
+            f2 z = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z = fma2(s[c][j], s[c][j], z);
+            q[0] += ring.live(c) ? sum2(z) : 0.f;
+            if (a.s_out && ring.live(c)) store_pairs<XB>(a.s_out, row + ring.col(c), s[c]);
+        }
+        if (a.o) {
+            block_sums<1>(q, tmp[1]);
+            const float r = rsqrtf(q[0] * inv_h + a.eps);
+            const f2 r2 = pair(r, r);
+#pragma unroll
+            for (int c = 0; c < kVpt; ++c) {
+                f2 w[4];
+                load_weights(w_pre, H, ring.wcol(c), w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = mul2(mul2(s[c][j], r2), w[j]);
+                if (ring.live(c)) store_pairs<OB>(a.o, row + ring.col(c), w);
+            }
+        }
+        if (!(a.o && a.post_w)) __syncthreads();  // one of the sums' places was not used
+    }
+}
+
+template <bool XB, bool YB, bool OB>
+__global__ void __launch_bounds__(kRingMaxThreads)
+block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
+                           const __grid_constant__ RingPlan p) {
+    extern __shared__ __align__(128) char smem[];
+    __shared__ float tmp[2][3 * 32];
+    const int H = a.H;
+    float* w_pre = reinterpret_cast<float*>(smem);
+    float* w_cp = w_pre + H;
+    const RowRing ring{p, smem + p.weights, H, a.T};
+    const float inv_h = 1.f / (float)H;
+    constexpr int kGo = 0, kS = 1, kGs = 2, kY = 3;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = 0; i < p.slots - 1; ++i)
+        ring.fetch<OB, XB, XB, YB>(blockIdx.x + (int64_t)i * gridDim.x, i);
+    stage_weights(w_pre, w_cp, a);
+    f2 c_pre[kVpt][4], c_y[kVpt][4];
+#pragma unroll
+    for (int c = 0; c < kVpt; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c_pre[c][j] = c_y[c][j] = 0;
+    int slot = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        cp_async_wait_n(p.slots - 2);
+        const int64_t row = t * H;
+        float q[3] = {0.f, 0.f, 0.f};  // sum s^2, sum do pre_w s, sum y^2
+#pragma unroll
+        for (int c = 0; c < kVpt; ++c) {
+            f2 z0 = 0, z1 = 0, z2 = 0;
+            if (a.go) {
+                f2 s[4], g[4], w[4];
+                ring.load<OB>(kGo, slot, c, g);
+                ring.load<XB>(kS, slot, c, s);
+                load_weights(w_pre, H, ring.wcol(c), w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    z0 = fma2(s[j], s[j], z0);
+                    z1 = fma2(mul2(g[j], s[j]), w[j], z1);
+                }
+            }
+            if (a.post_w) {
+                f2 y[4];
+                ring.load<YB>(kY, slot, c, y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z2 = fma2(y[j], y[j], z2);
+            }
+            if (ring.live(c)) {
+                q[0] += sum2(z0);
+                q[1] += sum2(z1);
+                q[2] += sum2(z2);
+            }
+        }
+        float gt = 1.f;
+        if (a.gate_kind == COLI_GATE_TOKEN) gt = __ldg(a.gate + t);
+        block_sums<3>(q, tmp[0]);
+        const float r = rsqrtf(q[0] * inv_h + a.eps);
+        const float ry = a.post_w ? rsqrtf(q[2] * inv_h + a.eps) : 1.f;
+        const float rk = -r * (r * r * (q[1] * inv_h));
+        const float A = a.alpha * gt, cy = gt * ry;
+        const f2 r2 = pair(r, r), rk2 = pair(rk, rk), cy2 = pair(cy, cy);
+        f2 e[kVpt][4];            // cp d
+        float sum[1] = {0.f};     // sum cp d y
+#pragma unroll
+        for (int c = 0; c < kVpt; ++c) {
+            f2 d[4] = {0, 0, 0, 0};
+            if (a.gs) ring.load<XB>(kGs, slot, c, d);
+            if (a.go) {
+                f2 s[4], g[4], w[4];
+                ring.load<OB>(kGo, slot, c, g);
+                ring.load<XB>(kS, slot, c, s);
+                load_weights(w_pre, H, ring.wcol(c), w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    c_pre[c][j] = fma2(mul2(g[j], s[j]), r2, c_pre[c][j]);
+                    d[j] = fma2(mul2(g[j], w[j]), r2, d[j]);
+                    d[j] = fma2(s[j], rk2, d[j]);
+                }
+            }
+            if (a.dx && ring.live(c)) store_pairs<XB>(a.dx, row + ring.col(c), d);
+            if (a.y) {
+                f2 y[4], w[4], z = 0;
+                ring.load<YB>(kY, slot, c, y);
+                load_weights(w_cp, H, ring.wcol(c), w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    c_y[c][j] = fma2(mul2(d[j], y[j]), cy2, c_y[c][j]);
+                    e[c][j] = mul2(d[j], w[j]);
+                    z = fma2(e[c][j], y[j], z);
+                }
+                sum[0] += ring.live(c) ? sum2(z) : 0.f;
+            }
+        }
+        if (a.y) {
+            block_sums<1>(sum, tmp[1]);
+            const float c1 = ry * A;
+            const float c2 = a.post_w ? -ry * (ry * ry * (A * sum[0] * inv_h)) : 0.f;
+            const f2 c12 = pair(c1, c1), c22 = pair(c2, c2);
+            if (a.dy) {
+#pragma unroll
+                for (int c = 0; c < kVpt; ++c) {
+                    f2 y[4];
+                    ring.load<YB>(kY, slot, c, y);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = fma2(c12, e[c][j], mul2(c22, y[j]));
+                    if (ring.live(c)) store_pairs<YB>(a.dy, row + ring.col(c), y);
+                }
+            }
+            if (a.dgate && a.gate_kind == COLI_GATE_TOKEN && threadIdx.x == 0)
+                a.dgate[t] = a.alpha * ry * sum[0];
+        } else {
+            __syncthreads();  // tmp[0] is read by all before the next row writes it
+        }
+        const int next = slot == 0 ? p.slots - 1 : slot - 1;
+        ring.fetch<OB, XB, XB, YB>(t + (int64_t)(p.slots - 1) * gridDim.x, next);
+        slot = slot + 1 == p.slots ? 0 : slot + 1;
+    }
+    if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * H;
+#pragma unroll
+    for (int c = 0; c < kVpt; ++c) {
+        if (!ring.live(c)) continue;
+        if (a.dpre_w) store_pairs<false>(part, ring.col(c), c_pre[c]);
+        if (a.y) store_pairs<false>(part + H, ring.col(c), c_y[c]);
+    }
+}
+
+// Column sums over the CTAs' partial rows, 32 columns per block, 8 warps over
+// the CTAs; fixed order (each warp its strided share ascending, then the warps
+// ascending).  blockIdx.y 0: dpre_w, 1: C, from which dpost_w and a channel
+// gate's dgate follow.
 __global__ void __launch_bounds__(256)
-norm_columns_kernel(const float* part, int n_part, int H, float* dpre_w, float* dpost_w,
-                    float* dgate) {
+norm_columns_kernel(const NormArgs a, int n_part) {
     __shared__ float acc[8][32];
     pdl_wait();
     pdl_launch_dependents();
-    const int which = blockIdx.y;
-    float* out = which == 0 ? dpre_w : which == 1 ? dpost_w : dgate;
-    if (!out) return;
+    const bool channel = a.gate_kind == COLI_GATE_CHANNEL;
+    float* dgate = channel ? a.dgate : nullptr;
+    if (blockIdx.y == 0 ? !a.dpre_w : !(a.dpost_w || dgate)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int h = blockIdx.x * 32 + lane;
     float v = 0.f;
-    if (h < H) {
-        const float* p = part + (int64_t)which * H + h;
+    if (h < a.H) {
+        const float* p = a.part + (int64_t)blockIdx.y * a.H + h;
 #pragma unroll 4
-        for (int i = warp; i < n_part; i += 8) v += p[(int64_t)i * 3 * H];
+        for (int i = warp; i < n_part; i += 8) v += p[(int64_t)i * 2 * a.H];
     }
     acc[warp][lane] = v;
     __syncthreads();
-    if (warp == 0 && h < H) {
+    if (warp != 0 || h >= a.H) return;
 #pragma unroll
-        for (int w = 1; w < 8; ++w) v += acc[w][lane];
-        out[h] = v;
+    for (int w = 1; w < 8; ++w) v += acc[w][lane];
+    if (blockIdx.y == 0) {
+        a.dpre_w[h] = v;
+    } else {
+        v *= a.alpha;
+        if (a.dpost_w) a.dpost_w[h] = channel ? v * a.gate[h] : v;
+        if (dgate) dgate[h] = a.post_w ? v * a.post_w[h] : v;
     }
 }
 
@@ -361,8 +745,65 @@ coli_status check_norm(int32_t T, int32_t H, int32_t gate_kind, const void* gate
     return COLI_OK;
 }
 
-// CTAs of the backward kernel: two per SM hide each other's row reductions.
-int norm_bwd_ctas(int T) { return std::max(1, std::min(T, 2 * 148)); }
+// CTAs of the backward kernels, at most (each leaves one partial row of column
+// sums in the workspace).
+constexpr int kMaxBwdCtas = 3 * 148;
+int norm_bwd_ctas(int T) { return std::max(1, std::min(T, kMaxBwdCtas)); }
+
+// Widths and rows per CTA from which the ring kernels pay: below them the
+// weights' way into shared memory costs more than the rows gain.
+constexpr int kRingMinH = 512, kRingRows = 3;
+
+// The ring kernels' launch for these arrays: threads, CTAs per SM and ring depth,
+// or false where the row is too wide, not of whole vectors, or the rows too few.
+bool plan_ring(const NormArgs& a, const void* const (&src)[4], const int (&bf16)[4], RingPlan* p,
+               int* threads, int* grid, int* smem) {
+    if (a.H % 8 || a.H < kRingMinH || a.H > 8 * kVpt * kRingMaxThreads) return false;
+    *threads = ((a.H + 8 * kVpt - 1) / (8 * kVpt) + 31) / 32 * 32;
+    *p = RingPlan{};
+    uint32_t slot = 0;
+    for (int k = 0; k < 4; ++k) {
+        if (!src[k]) continue;
+        p->src[k] = src[k];
+        p->at[k] = slot;
+        slot += (uint32_t)(*threads * 8 * kVpt) * (bf16[k] ? 2 : 4);
+    }
+    p->slot = (slot + 127) / 128 * 128;
+    p->weights = (uint32_t)(2 * sizeof(float) * a.H + 127) / 128 * 128;
+    for (int per_sm = std::max(1, std::min(3, 1024 / *threads)); per_sm >= 1; --per_sm) {
+        const int budget = 224 * 1024 / per_sm - 2048;
+        const int slots = std::min(8, (budget - (int)p->weights) / (int)p->slot);
+        if (slots < (per_sm == 1 ? 2 : 3)) continue;
+        p->slots = slots;
+        *grid = 148 * per_sm;
+        *smem = (int)(p->weights + slots * p->slot);
+        if (a.T < *grid * kRingRows) continue;
+        return true;
+    }
+    return false;
+}
+
+template <bool XB, bool YB, bool OB>
+cudaError_t launch_ring(bool backward, const NormArgs& a, const RingPlan& p, int threads, int grid,
+                        int smem, cudaStream_t st) {
+    auto kernel =
+        backward ? block_norm_bwd_ring_kernel<XB, YB, OB> : block_norm_ring_kernel<XB, YB, OB>;
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    return launch_serialized(kernel, dim3(grid), dim3(threads), smem, st, a, p);
+}
+
+cudaError_t dispatch_ring(bool backward, const NormArgs& a, const RingPlan& p, int threads, int grid,
+                          int smem, cudaStream_t st) {
+    using Fn = cudaError_t (*)(bool, const NormArgs&, const RingPlan&, int, int, int, cudaStream_t);
+    static const Fn fn[2][2][2] = {
+        {{launch_ring<false, false, false>, launch_ring<false, false, true>},
+         {launch_ring<false, true, false>, launch_ring<false, true, true>}},
+        {{launch_ring<true, false, false>, launch_ring<true, false, true>},
+         {launch_ring<true, true, false>, launch_ring<true, true, true>}}};
+    return fn[a.x_bf16 != 0][a.y_bf16 != 0][a.o_bf16 != 0](backward, a, p, threads, grid, smem, st);
+}
 
 // Chunks per thread: rows of whole 8-value vectors use 16-byte accesses, other
 // widths one value at a time.
@@ -421,14 +862,22 @@ coli_status coli_moe_block_norm(int32_t T, int32_t H, const void* x, coli_out_dt
     a.y_bf16 = y_dtype == COLI_OUT_BF16;
     a.o_bf16 = o_dtype == COLI_OUT_BF16;
     a.s_out = s_out; a.o = o;
-    const cudaError_t err =
-        dispatch_width<Forward>(H, T <= 148 ? 1024 : 512, a, T, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const void* const src[4] = {x, y, nullptr, nullptr};
+    const int bf16[4] = {a.x_bf16, a.y_bf16, 0, 0};
+    RingPlan p;
+    int threads, grid, smem;
+    cudaError_t err;
+    if (plan_ring(a, src, bf16, &p, &threads, &grid, &smem))
+        err = dispatch_ring(false, a, p, threads, grid, smem, st);
+    else
+        err = dispatch_width<Forward>(H, T <= 148 ? 1024 : 512, a, T, st);
     return err == cudaSuccess ? COLI_OK : COLI_ERR_CUDA;
 }
 
 size_t coli_moe_block_norm_workspace_size(int32_t T, int32_t H) {
     if (T < 0 || H <= 0) return 0;
-    return kHeaderBytes + sizeof(float) * 3 * (size_t)H * (size_t)norm_bwd_ctas(T);
+    return kHeaderBytes + sizeof(float) * 2 * (size_t)H * (size_t)norm_bwd_ctas(T);
 }
 
 coli_status coli_moe_block_norm_backward(
@@ -472,12 +921,20 @@ coli_status coli_moe_block_norm_backward(
     a.go = go; a.gs = gs; a.s = s_in; a.dx = dx; a.dy = dy;
     a.dpre_w = dpre_w; a.dpost_w = dpost_w; a.dgate = dgate;
     a.part = columns ? reinterpret_cast<float*>(static_cast<char*>(ws) + kHeaderBytes) : nullptr;
-    const int grid = norm_bwd_ctas(T);
-    cudaError_t err = dispatch_width<Backward>(H, 512, a, grid, st);
+    const void* const src[4] = {go, go ? s_in : nullptr, gs, y};
+    const int bf16[4] = {a.o_bf16, a.x_bf16, a.x_bf16, a.y_bf16};
+    RingPlan p;
+    int threads, smem, grid;
+    cudaError_t err;
+    if (plan_ring(a, src, bf16, &p, &threads, &grid, &smem)) {
+        err = dispatch_ring(true, a, p, threads, grid, smem, st);
+    } else {
+        grid = std::min(norm_bwd_ctas(T), 2 * 148);
+        err = dispatch_width<Backward>(H, 512, a, grid, st);
+    }
     if (err == cudaSuccess && columns)
-        err = launch_serialized(norm_columns_kernel, dim3((H + 31) / 32, 3), dim3(256), 0, st,
-                                a.part, grid, H, dpre_w, dpost_w,
-                                gate_kind == COLI_GATE_CHANNEL ? dgate : nullptr);
+        err = launch_serialized(norm_columns_kernel, dim3((H + 31) / 32, 2), dim3(256), 0, st, a,
+                                grid);
     return err == cudaSuccess ? COLI_OK : COLI_ERR_CUDA;
 }
 
