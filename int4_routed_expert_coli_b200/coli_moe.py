@@ -267,24 +267,29 @@ _DTYPE = {torch.float32: COLI_OUT_F32, torch.bfloat16: COLI_OUT_BF16}
 
 
 def _arg(t, name, numel, dtypes, device, optional=False):
-    """Pointer of a checked tensor argument (None for an absent optional one)."""
+    """Address of a checked tensor argument on CUDA device `device` (None for
+    an absent optional one)."""
+    if t is None and optional:
+        return None
+    try:  # one pass over what a right argument satisfies
+        if (t.get_device() == device and t.dtype in dtypes and t.numel() == numel
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is missing")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on the CUDA device")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, other arguments on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, other arguments on cuda:{device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: type {t.dtype} is not one of {tuple(dtypes)}")
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
-    if t.numel() != numel:
-        raise ValueError(f"{name} has {t.numel()} elements, the call's sizes need {numel}")
-    return t.data_ptr()
+    raise ValueError(f"{name} has {t.numel()} elements, the call's sizes need {numel}")
 
 
 _F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
@@ -292,20 +297,26 @@ _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
 def _device(*tensors):
+    """Index of the CUDA device of the first tensor given."""
     for t in tensors:
         if isinstance(t, torch.Tensor):
-            return t.device
+            if not t.is_cuda:
+                raise ValueError("tensor arguments must live on the CUDA device")
+            return t.get_device()
     raise ValueError("no tensor argument")
 
 
 def _run(fn, device, stream, *args):
-    """fn(*args, stream) on `device`."""
-    if device.type != "cuda":
-        raise ValueError("tensor arguments must live on the CUDA device")
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
+    """fn(*args, stream) on `device`, by default on its current stream."""
+    current = torch.cuda.current_device()
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if device == current:
+        return fn(*args, handle)
     with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+        return fn(*args, handle)
 
 
 def _ws_arg(ws, device):
@@ -313,7 +324,7 @@ def _ws_arg(ws, device):
     if ws is None:
         return None, 0
     n = ws.numel()
-    return _arg(ws, "ws", n, (ws.dtype,), device), n * ws.element_size()
+    return _arg(ws, "ws", n, (ws.dtype,), device), ws.nbytes
 
 
 def coli_moe_block_norm(T, H, x, y, post_w, gate, gate_kind, alpha, pre_w, eps, s_out, o,

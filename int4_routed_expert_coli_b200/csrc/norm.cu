@@ -323,13 +323,47 @@ block_norm_bwd_kernel(const NormArgs a) {
 // of 8 columns and copies them (cp.async) into its own places of a ring in
 // shared memory, rows ahead of the one it works on, so that the memory system
 // has rows in flight whatever the row reductions wait for; nobody else reads
-// those places, so the copies need no barrier.  The weights lie in shared
-// memory too: read from L2 for every row they would be more bytes than the row
-// itself.  The types are template parameters and the loops have no branches
+// those places, so the copies need no barrier.  The weights of
+// a thread's columns lie in its registers (384 threads, H 6144) or in shared
+// memory (wider rows): read from L2 for every row they would be more bytes
+// than the row itself.  The types are template parameters and the loops have no branches
 // (a vector past the row's end has places of its own that nothing fills;
 // its sums are masked and its stores left out), so that a row's loads and sums interleave.
 constexpr int kVpt = 2;                 // vectors per thread
 constexpr int kRingMaxThreads = 512;
+constexpr int kRegThreads = 384;        // up to these, the weights fit in registers
+
+// Block sums of N = 2 or 4 values over at most 16 warps, in a fixed order.  The
+// first levels of the butterfly halve the values a lane carries instead of
+// reducing each of them: N - 1 + 5 - log2(N) shuffles a stage and not 5 N.
+template <int N>
+__device__ __forceinline__ void ring_sums(float (&v)[N], float* tmp) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    float x;
+    if constexpr (N == 4) {
+        const bool b0 = lane & 1, b1 = lane & 2;
+        const float k0 = (b0 ? v[1] : v[0]) + __shfl_xor_sync(kAll, b0 ? v[0] : v[1], 1);
+        const float k1 = (b0 ? v[3] : v[2]) + __shfl_xor_sync(kAll, b0 ? v[2] : v[3], 1);
+        x = (b1 ? k1 : k0) + __shfl_xor_sync(kAll, b1 ? k0 : k1, 2);
+    } else {
+        const bool b0 = lane & 1;
+        x = (b0 ? v[1] : v[0]) + __shfl_xor_sync(kAll, b0 ? v[0] : v[1], 1);
+    }
+#pragma unroll
+    for (int o = N; o < 32; o <<= 1) x += __shfl_xor_sync(kAll, x, o);
+    if (lane < N) tmp[lane * 32 + warp] = x;  // value `lane` of this warp
+    __syncthreads();
+    // 32 / N lanes to a value, each with its share of the warps
+    constexpr int kLanes = 32 / N;
+    const int k = lane / kLanes, i = lane % kLanes;
+    x = i < nw ? tmp[k * 32 + i] : 0.f;
+    if (kLanes < 16 && i + kLanes < nw) x += tmp[k * 32 + i + kLanes];
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) x += __shfl_xor_sync(kAll, x, o);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = __shfl_sync(kAll, x, j * kLanes);
+}
 
 // Pairs of fp32 values in one 64-bit register: one instruction for both.  (Issue
 // slots bound the scalar form: 52 and 91 us at 4096 x 6144 bf16.)
@@ -405,7 +439,7 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
                  : "memory");
 }
-// At most `n` of this thread's latest groups in flight (n < 7).
+// At most `n` of this thread's latest groups in flight (n <= 6).
 __device__ __forceinline__ void cp_async_wait_n(int n) {
     switch (n) {
         case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
@@ -429,8 +463,6 @@ struct RowRing {
         return (c * blockDim.x + threadIdx.x) * 8;
     }
     __device__ __forceinline__ bool live(int c) const { return col(c) < H; }
-    // the same, clamped to the row (weights)
-    __device__ __forceinline__ int wcol(int c) const { return min(col(c), H - 8); }
 
     template <bool BF16>
     __device__ __forceinline__ void copy(int k, int64_t t, char* slot) const {
@@ -489,57 +521,107 @@ __device__ __forceinline__ void load_weights(const float* w, int H, int col, f2 
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-template <bool XB, bool YB, bool OB>
-__global__ void __launch_bounds__(kRingMaxThreads)
+// A thread's weights (pre_w, and post_w times a channel's gate), in registers or
+// in shared memory.
+template <bool REG>
+struct Weights {
+    f2 v[REG ? 2 : 1][REG ? kVpt : 1][4];
+    const float* at;
+    int H;
+
+    __device__ __forceinline__ Weights(const NormArgs& a, char* smem)
+        : at(reinterpret_cast<const float*>(smem)), H(a.H) {
+        if constexpr (REG) {
+#pragma unroll
+            for (int c = 0; c < kVpt; ++c) {
+                const int h = min(RowRing::col(c), a.H - 8);
+                float w[8], g[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 1.f;
+                if (a.pre_w) load_vals<8>(a.pre_w, h, 0, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[0][c][j] = pair(w[2 * j], w[2 * j + 1]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 1.f;
+                if (a.post_w) load_vals<8>(a.post_w, h, 0, w);
+                if (a.gate_kind == COLI_GATE_CHANNEL) {
+                    load_vals<8>(a.gate, h, 0, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] *= g[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[1][c][j] = pair(w[2 * j], w[2 * j + 1]);
+            }
+        } else {
+            stage_weights(reinterpret_cast<float*>(smem), reinterpret_cast<float*>(smem) + H, a);
+        }
+    }
+    // k 0: pre_w, 1: post_w times the gate
+    __device__ __forceinline__ void load(int k, int c, f2 (&w)[4]) const {
+        if constexpr (REG) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = v[k][c][j];
+        } else {
+            load_weights(at + k * H, H, min(RowRing::col(c), H - 8), w);
+        }
+    }
+};
+
+template <bool REG, bool XB, bool YB, bool OB>
+__global__ void __launch_bounds__(REG ? kRegThreads : kRingMaxThreads)
 block_norm_ring_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ RingPlan p) {
     extern __shared__ __align__(128) char smem[];
-    __shared__ float tmp[2][32];
+    __shared__ float tmp[2][2 * 32];
     const int H = a.H;
-    float* w_pre = reinterpret_cast<float*>(smem);
-    float* w_cp = w_pre + H;
     const RowRing ring{p, smem + p.weights, H, a.T};
     const float inv_h = 1.f / (float)H;
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = 0; i < p.slots - 1; ++i)
+    for (int i = 0; i < p.slots; ++i)
         ring.fetch<XB, YB, false, false>(blockIdx.x + (int64_t)i * gridDim.x, i);
-    stage_weights(w_pre, w_cp, a);
-    int slot = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        cp_async_wait_n(p.slots - 2);
-        const int64_t row = t * H;
-        f2 s[kVpt][4], y[kVpt][4];
-        float q[1] = {0.f};
+    const Weights<REG> weights(a, smem);
+    // this thread's share of the sum of y^2 of the row in slot i
+    auto sum_y = [&](int i) {
+        float q = 0.f;
 #pragma unroll
         for (int c = 0; c < kVpt; ++c) {
-            ring.load<XB>(0, slot, c, s[c]);
-            if (a.y) ring.load<YB>(1, slot, c, y[c]);
-            if (a.post_w) {
-                f2 z = 0;
+            f2 y[4], z = 0;
+            ring.load<YB>(1, i, c, y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) z = fma2(y[c][j], y[c][j], z);
-                q[0] += ring.live(c) ? sum2(z) : 0.f;
-            }
+            for (int j = 0; j < 4; ++j) z = fma2(y[j], y[j], z);
+            q += ring.live(c) ? sum2(z) : 0.f;
         }
-        {   // the slot is in registers: fetch the row that takes the place before it
-            const int next = slot == 0 ? p.slots - 1 : slot - 1;
-            ring.fetch<XB, YB, false, false>(t + (int64_t)(p.slots - 1) * gridDim.x, next);
-            slot = slot + 1 == p.slots ? 0 : slot + 1;
-        }
+        return q;
+    };
+    // One round of block sums a row: the y^2 of the next row joins the s^2 of
+    // this one.
+    float q[2] = {0.f, 0.f};
+    if (a.post_w) {
+        cp_async_wait_n(p.slots - 1);
+        q[1] = sum_y(0);
+        ring_sums<2>(q, tmp[1]);
+    }
+    int slot = 0, odd = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        // this row and the next one are in the ring
+        cp_async_wait_n(p.slots - 2);
+        const int64_t row = t * H;
+        const int after = slot + 1 == p.slots ? 0 : slot + 1;
+        f2 s[kVpt][4];
+#pragma unroll
+        for (int c = 0; c < kVpt; ++c) ring.load<XB>(0, slot, c, s[c]);
         if (a.y) {
             float A = a.alpha;
             if (a.gate_kind == COLI_GATE_TOKEN) A *= __ldg(a.gate + t);
-            if (a.post_w) {
-                block_sums<1>(q, tmp[0]);
-                A *= rsqrtf(q[0] * inv_h + a.eps);
-            }
+            if (a.post_w) A *= rsqrtf(q[1] * inv_h + a.eps);
             const f2 A2 = pair(A, A);
 #pragma unroll
             for (int c = 0; c < kVpt; ++c) {
-                f2 w[4];
-                load_weights(w_cp, H, ring.wcol(c), w);
+                f2 y[4], w[4];
+                ring.load<YB>(1, slot, c, y);
+                weights.load(1, c, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[c][j] = fma2(A2, mul2(y[c][j], w[j]), s[c][j]);
+                for (int j = 0; j < 4; ++j) s[c][j] = fma2(A2, mul2(y[j], w[j]), s[c][j]);
             }
         }
         q[0] = 0.f;
@@ -551,58 +633,59 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, const __grid_constant
             q[0] += ring.live(c) ? sum2(z) : 0.f;
             if (a.s_out && ring.live(c)) store_pairs<XB>(a.s_out, row + ring.col(c), s[c]);
         }
+        q[1] = a.post_w ? sum_y(after) : 0.f;
+        // the slot is read: fetch the row that takes its place
+        ring.fetch<XB, YB, false, false>(t + (int64_t)p.slots * gridDim.x, slot);
+        if (a.o || a.post_w) ring_sums<2>(q, tmp[odd]);
         if (a.o) {
-            block_sums<1>(q, tmp[1]);
             const float r = rsqrtf(q[0] * inv_h + a.eps);
             const f2 r2 = pair(r, r);
 #pragma unroll
             for (int c = 0; c < kVpt; ++c) {
                 f2 w[4];
-                load_weights(w_pre, H, ring.wcol(c), w);
+                weights.load(0, c, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = mul2(mul2(s[c][j], r2), w[j]);
                 if (ring.live(c)) store_pairs<OB>(a.o, row + ring.col(c), w);
             }
         }
-        if (!(a.o && a.post_w)) __syncthreads();  // one of the sums' places was not used
+        slot = after;
+        odd ^= 1;
     }
 }
 
-template <bool XB, bool YB, bool OB>
-__global__ void __launch_bounds__(kRingMaxThreads)
+template <bool REG, bool XB, bool YB, bool OB>
+__global__ void __launch_bounds__(REG ? kRegThreads : kRingMaxThreads)
 block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
                            const __grid_constant__ RingPlan p) {
     extern __shared__ __align__(128) char smem[];
-    __shared__ float tmp[2][3 * 32];
+    __shared__ float tmp[2][4 * 32];
     const int H = a.H;
-    float* w_pre = reinterpret_cast<float*>(smem);
-    float* w_cp = w_pre + H;
     const RowRing ring{p, smem + p.weights, H, a.T};
     const float inv_h = 1.f / (float)H;
     constexpr int kGo = 0, kS = 1, kGs = 2, kY = 3;
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = 0; i < p.slots - 1; ++i)
+    for (int i = 0; i < p.slots; ++i)
         ring.fetch<OB, XB, XB, YB>(blockIdx.x + (int64_t)i * gridDim.x, i);
-    stage_weights(w_pre, w_cp, a);
+    const Weights<REG> weights(a, smem);
     f2 c_pre[kVpt][4], c_y[kVpt][4];
 #pragma unroll
     for (int c = 0; c < kVpt; ++c)
 #pragma unroll
         for (int j = 0; j < 4; ++j) c_pre[c][j] = c_y[c][j] = 0;
-    int slot = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        cp_async_wait_n(p.slots - 2);
-        const int64_t row = t * H;
-        float q[3] = {0.f, 0.f, 0.f};  // sum s^2, sum do pre_w s, sum y^2
+    // This thread's shares of the first three sums of the row in slot i: s^2,
+    // do pre_w s, y^2.
+    auto first_sums = [&](int i, float (&q)[4]) {
+        q[0] = q[1] = q[2] = 0.f;
 #pragma unroll
         for (int c = 0; c < kVpt; ++c) {
             f2 z0 = 0, z1 = 0, z2 = 0;
             if (a.go) {
                 f2 s[4], g[4], w[4];
-                ring.load<OB>(kGo, slot, c, g);
-                ring.load<XB>(kS, slot, c, s);
-                load_weights(w_pre, H, ring.wcol(c), w);
+                ring.load<OB>(kGo, i, c, g);
+                ring.load<XB>(kS, i, c, s);
+                weights.load(0, c, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     z0 = fma2(s[j], s[j], z0);
@@ -611,7 +694,7 @@ block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
             }
             if (a.post_w) {
                 f2 y[4];
-                ring.load<YB>(kY, slot, c, y);
+                ring.load<YB>(kY, i, c, y);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) z2 = fma2(y[j], y[j], z2);
             }
@@ -621,16 +704,29 @@ block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
                 q[2] += sum2(z2);
             }
         }
+    };
+    // One round of block sums a row: the next row's first three join this row's
+    // last.
+    float q[4];
+    cp_async_wait_n(p.slots - 1);
+    first_sums(0, q);
+    q[3] = 0.f;
+    ring_sums<4>(q, tmp[1]);
+    int slot = 0, odd = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        // this row and the next one are in the ring
+        cp_async_wait_n(p.slots - 2);
+        const int64_t row = t * H;
+        const int after = slot + 1 == p.slots ? 0 : slot + 1;
         float gt = 1.f;
         if (a.gate_kind == COLI_GATE_TOKEN) gt = __ldg(a.gate + t);
-        block_sums<3>(q, tmp[0]);
         const float r = rsqrtf(q[0] * inv_h + a.eps);
         const float ry = a.post_w ? rsqrtf(q[2] * inv_h + a.eps) : 1.f;
         const float rk = -r * (r * r * (q[1] * inv_h));
         const float A = a.alpha * gt, cy = gt * ry;
         const f2 r2 = pair(r, r), rk2 = pair(rk, rk), cy2 = pair(cy, cy);
         f2 e[kVpt][4];            // cp d
-        float sum[1] = {0.f};     // sum cp d y
+        q[3] = 0.f;               // sum cp d y
 #pragma unroll
         for (int c = 0; c < kVpt; ++c) {
             f2 d[4] = {0, 0, 0, 0};
@@ -639,7 +735,7 @@ block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
                 f2 s[4], g[4], w[4];
                 ring.load<OB>(kGo, slot, c, g);
                 ring.load<XB>(kS, slot, c, s);
-                load_weights(w_pre, H, ring.wcol(c), w);
+                weights.load(0, c, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     c_pre[c][j] = fma2(mul2(g[j], s[j]), r2, c_pre[c][j]);
@@ -651,20 +747,21 @@ block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
             if (a.y) {
                 f2 y[4], w[4], z = 0;
                 ring.load<YB>(kY, slot, c, y);
-                load_weights(w_cp, H, ring.wcol(c), w);
+                weights.load(1, c, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     c_y[c][j] = fma2(mul2(d[j], y[j]), cy2, c_y[c][j]);
                     e[c][j] = mul2(d[j], w[j]);
                     z = fma2(e[c][j], y[j], z);
                 }
-                sum[0] += ring.live(c) ? sum2(z) : 0.f;
+                q[3] += ring.live(c) ? sum2(z) : 0.f;
             }
         }
+        first_sums(after, q);
+        ring_sums<4>(q, tmp[odd]);
         if (a.y) {
-            block_sums<1>(sum, tmp[1]);
             const float c1 = ry * A;
-            const float c2 = a.post_w ? -ry * (ry * ry * (A * sum[0] * inv_h)) : 0.f;
+            const float c2 = a.post_w ? -ry * (ry * ry * (A * q[3] * inv_h)) : 0.f;
             const f2 c12 = pair(c1, c1), c22 = pair(c2, c2);
             if (a.dy) {
 #pragma unroll
@@ -677,13 +774,11 @@ block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
                 }
             }
             if (a.dgate && a.gate_kind == COLI_GATE_TOKEN && threadIdx.x == 0)
-                a.dgate[t] = a.alpha * ry * sum[0];
-        } else {
-            __syncthreads();  // tmp[0] is read by all before the next row writes it
+                a.dgate[t] = a.alpha * ry * q[3];
         }
-        const int next = slot == 0 ? p.slots - 1 : slot - 1;
-        ring.fetch<OB, XB, XB, YB>(t + (int64_t)(p.slots - 1) * gridDim.x, next);
-        slot = slot + 1 == p.slots ? 0 : slot + 1;
+        ring.fetch<OB, XB, XB, YB>(t + (int64_t)p.slots * gridDim.x, slot);
+        slot = after;
+        odd ^= 1;
     }
     if (!a.part) return;
     float* part = a.part + (int64_t)blockIdx.x * 2 * H;
@@ -769,11 +864,12 @@ bool plan_ring(const NormArgs& a, const void* const (&src)[4], const int (&bf16)
         slot += (uint32_t)(*threads * 8 * kVpt) * (bf16[k] ? 2 : 4);
     }
     p->slot = (slot + 127) / 128 * 128;
-    p->weights = (uint32_t)(2 * sizeof(float) * a.H + 127) / 128 * 128;
-    for (int per_sm = std::max(1, std::min(3, 1024 / *threads)); per_sm >= 1; --per_sm) {
+    p->weights =
+        *threads <= kRegThreads ? 0 : (uint32_t)(2 * sizeof(float) * a.H + 127) / 128 * 128;
+    for (int per_sm = std::max(1, std::min(3, 768 / *threads)); per_sm >= 1; --per_sm) {
         const int budget = 224 * 1024 / per_sm - 2048;
-        const int slots = std::min(8, (budget - (int)p->weights) / (int)p->slot);
-        if (slots < (per_sm == 1 ? 2 : 3)) continue;
+        const int slots = std::min(7, (budget - (int)p->weights) / (int)p->slot);
+        if (slots < 3) continue;  // two rows in hand, one on its way
         p->slots = slots;
         *grid = 148 * per_sm;
         *smem = (int)(p->weights + slots * p->slot);
@@ -783,25 +879,26 @@ bool plan_ring(const NormArgs& a, const void* const (&src)[4], const int (&bf16)
     return false;
 }
 
-template <bool XB, bool YB, bool OB>
+template <bool REG, bool XB, bool YB, bool OB>
 cudaError_t launch_ring(bool backward, const NormArgs& a, const RingPlan& p, int threads, int grid,
                         int smem, cudaStream_t st) {
-    auto kernel =
-        backward ? block_norm_bwd_ring_kernel<XB, YB, OB> : block_norm_ring_kernel<XB, YB, OB>;
+    auto kernel = backward ? block_norm_bwd_ring_kernel<REG, XB, YB, OB>
+                           : block_norm_ring_kernel<REG, XB, YB, OB>;
     const cudaError_t err =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     return launch_serialized(kernel, dim3(grid), dim3(threads), smem, st, a, p);
 }
 
+template <bool REG>
 cudaError_t dispatch_ring(bool backward, const NormArgs& a, const RingPlan& p, int threads, int grid,
                           int smem, cudaStream_t st) {
     using Fn = cudaError_t (*)(bool, const NormArgs&, const RingPlan&, int, int, int, cudaStream_t);
     static const Fn fn[2][2][2] = {
-        {{launch_ring<false, false, false>, launch_ring<false, false, true>},
-         {launch_ring<false, true, false>, launch_ring<false, true, true>}},
-        {{launch_ring<true, false, false>, launch_ring<true, false, true>},
-         {launch_ring<true, true, false>, launch_ring<true, true, true>}}};
+        {{launch_ring<REG, false, false, false>, launch_ring<REG, false, false, true>},
+         {launch_ring<REG, false, true, false>, launch_ring<REG, false, true, true>}},
+        {{launch_ring<REG, true, false, false>, launch_ring<REG, true, false, true>},
+         {launch_ring<REG, true, true, false>, launch_ring<REG, true, true, true>}}};
     return fn[a.x_bf16 != 0][a.y_bf16 != 0][a.o_bf16 != 0](backward, a, p, threads, grid, smem, st);
 }
 
@@ -869,7 +966,8 @@ coli_status coli_moe_block_norm(int32_t T, int32_t H, const void* x, coli_out_dt
     int threads, grid, smem;
     cudaError_t err;
     if (plan_ring(a, src, bf16, &p, &threads, &grid, &smem))
-        err = dispatch_ring(false, a, p, threads, grid, smem, st);
+        err = (threads <= kRegThreads ? dispatch_ring<true> : dispatch_ring<false>)(
+            false, a, p, threads, grid, smem, st);
     else
         err = dispatch_width<Forward>(H, T <= 148 ? 1024 : 512, a, T, st);
     return err == cudaSuccess ? COLI_OK : COLI_ERR_CUDA;
@@ -927,9 +1025,10 @@ coli_status coli_moe_block_norm_backward(
     int threads, smem, grid;
     cudaError_t err;
     if (plan_ring(a, src, bf16, &p, &threads, &grid, &smem)) {
-        err = dispatch_ring(true, a, p, threads, grid, smem, st);
+        err = (threads <= kRegThreads ? dispatch_ring<true> : dispatch_ring<false>)(
+            true, a, p, threads, grid, smem, st);
     } else {
-        grid = std::min(norm_bwd_ctas(T), 2 * 148);
+        grid = norm_bwd_ctas(T);
         err = dispatch_width<Backward>(H, 512, a, grid, st);
     }
     if (err == cudaSuccess && columns)
