@@ -67,6 +67,14 @@ constexpr int kMinRange = 12, kCutCost = 12;
 constexpr int kBand = 8;
 constexpr int kStoreBytes = 32 * 128;  // kDw: staging of one warp's stores
 
+// Tensor maps of a call.  An MN-major operand is copied 64 columns at a time
+// (a[0], b[0]), or 128 at once where its rows are whole runs of 64 columns
+// (a[1], b[1]: the runs are a dimension of their own); b[i] of a K-major one has
+// boxes of (i + 1) kBoxRows rows.
+struct Maps {
+    CUtensorMap a[2], b[4], out;
+};
+
 struct MmArgs {
     const int* offsets;   // [E + 1]
     int R, E;
@@ -75,6 +83,7 @@ struct MmArgs {
     int cols;             // kDw: columns of dw
     void* out;
     int out_bf16, accumulate;
+    int a_wide, b_wide;   // maps a[1], b[1] exist (MN-major operands)
     const float* xs;      // fp8: [KB][R] scales of the rows
     const float* ws;      // fp8: [E][ceil(M/128)][KB] scales of the weights
     float* part;          // partial tiles, two per CTA
@@ -90,9 +99,11 @@ struct Cfg {
     static constexpr int BN = BN_, CTAS = CTAS_;
     static constexpr int BK = FP8 ? 128 : 64;              // reduction per stage
     static constexpr bool kRows = MODE == kFwdRows;
-    // rows per B tensor copy, and of the copies of whole parts
+    // A part of B is loaded by one tensor copy of its rows rounded up to this: a
+    // box of 1 .. kBoxes times as many rows (each copy costs the loading thread
+    // about 25 ns: with boxes of 32 rows alone 8192 x 6144 x 6144 took 4 % longer).
     static constexpr int kBoxRows = kRows ? 128 : BN == 256 ? 32 : 16;
-    static constexpr int kBigBox = BN == 256 ? 128 : 64;
+    static constexpr int kBoxes = std::min(4, BN / CTAS / kBoxRows);
     static constexpr int kBBytes = BN / CTAS * kRowBytes;
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kTmemCols = 2 * BN;
@@ -335,10 +346,7 @@ __device__ __forceinline__ void drain(uint32_t src, const float* sc, float one, 
 
 template <int MODE, bool FP8, int BN_, int CTAS_>
 __global__ void __launch_bounds__(Cfg<MODE, FP8, BN_, CTAS_>::kThreads, 1)
-grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
-                  const __grid_constant__ CUtensorMap bmap,
-                  const __grid_constant__ CUtensorMap bmap_big,
-                  const __grid_constant__ CUtensorMap omap, const MmArgs a) {
+grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
     using C = Cfg<MODE, FP8, BN_, CTAS_>;
     constexpr int kStages = stage_count<C>();
     constexpr int CTAS = C::CTAS;
@@ -373,8 +381,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
     }
     if (warp == 1) tc::alloc<CTAS>(&s.tmem, C::kTmemCols);
     if (threadIdx.x == 0) {
-        tc::prefetch_map(&amap);
-        tc::prefetch_map(&bmap);
+        tc::prefetch_map(&maps.a[0]);
+        tc::prefetch_map(&maps.b[0]);
     }
     __syncthreads();
     pdl_launch_dependents();
@@ -462,7 +470,8 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                 uint32_t it = 0;
                 uint32_t tails = 0;   // parity of the next use of each stage's tail barrier
                 int last_tail = -1;
-                // boxes and bytes of one K-block of CTA `r` of the pair
+                // rows of B (kDw: columns, in runs of 64) that CTA `r` of the pair
+                // loads, in boxes
                 auto boxes_of = [&](int r) {
                     const int half = mma_n<C>(p.n) / CTAS;
                     const int n = max(0, min(half, p.n - r * half));
@@ -505,37 +514,40 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                             bar = CTAS == 2 ? tc::cluster_addr(&s.full[i], 0)
                                             : smem_addr(&s.full[i]);
                         }
+                        const int k = kb * C::BK;
                         if constexpr (MODE == kFwd) {
-                            tc::tma_3d<CTAS>(sa, &amap, kb * C::BK, p.m0, p.e, bar);
+                            tc::tma_3d<CTAS>(sa, &maps.a[0], k, p.m0, p.e, bar);
                         } else if constexpr (C::kRows) {
-                            tc::tma_2d<CTAS>(sa, &amap, kb * C::BK, p.row0, bar);
+                            tc::tma_2d<CTAS>(sa, &maps.a[0], k, p.row0, bar);
                         } else if constexpr (MODE == kDx) {
-                            tc::tma_3d<CTAS>(sa, &amap, p.m0, kb * C::BK, p.e, bar);
-                            tc::tma_3d<CTAS>(sa + kABytes / 2, &amap, p.m0 + 64, kb * C::BK, p.e,
-                                             bar);
+                            if (a.a_wide) {
+                                tc::tma_4d<CTAS>(sa, &maps.a[1], 0, k, p.m0 / 64, p.e, bar);
+                            } else {
+                                tc::tma_3d<CTAS>(sa, &maps.a[0], p.m0, k, p.e, bar);
+                                tc::tma_3d<CTAS>(sa + kABytes / 2, &maps.a[0], p.m0 + 64, k, p.e,
+                                                 bar);
+                            }
+                        } else if (a.a_wide) {
+                            tc::tma_3d<CTAS>(sa, &maps.a[1], 0, p.row0 + k, p.m0 / 64, bar);
                         } else {
-                            const int r = p.row0 + kb * C::BK;
-                            tc::tma_2d<CTAS>(sa, &amap, p.m0, r, bar);
-                            tc::tma_2d<CTAS>(sa + kABytes / 2, &amap, p.m0 + 64, r, bar);
+                            tc::tma_2d<CTAS>(sa, &maps.a[0], p.m0, p.row0 + k, bar);
+                            tc::tma_2d<CTAS>(sa + kABytes / 2, &maps.a[0], p.m0 + 64, p.row0 + k,
+                                             bar);
                         }
                         if constexpr (MODE == kDw) {
-                            for (int b = 0; b < boxes; ++b)
-                                tc::tma_2d<CTAS>(sb + b * 64 * kRowBytes, &bmap,
-                                                 p.col0 + b0 + b * 64, p.row0 + kb * C::BK, bar);
-                        } else if constexpr (C::kRows) {
-                            for (int b = 0; b < boxes; ++b)
-                                tc::tma_3d<CTAS>(sb + b * C::kBoxRows * kRowBytes, &bmap,
-                                                 kb * C::BK, p.col0 + b0 + b * C::kBoxRows, p.e,
-                                                 bar);
-                        } else {
-                            constexpr int kPer = C::kBigBox / C::kBoxRows;
-                            int b = 0;
-                            for (; b + kPer <= boxes; b += kPer)
-                                tc::tma_2d<CTAS>(sb + b * C::kBoxRows * kRowBytes, &bmap_big,
-                                                 kb * C::BK, p.row0 + b0 + b * C::kBoxRows, bar);
-                            for (; b < boxes; ++b)
-                                tc::tma_2d<CTAS>(sb + b * C::kBoxRows * kRowBytes, &bmap,
-                                                 kb * C::BK, p.row0 + b0 + b * C::kBoxRows, bar);
+                            // (a cut last tile's parts need not start at a run of 64)
+                            if (a.b_wide && p.n == C::BN)
+                                tc::tma_3d<CTAS>(sb, &maps.b[1], 0, p.row0 + k,
+                                                 (p.col0 + b0) / 64, bar);
+                            else
+                                for (int b = 0; b < boxes; ++b)
+                                    tc::tma_2d<CTAS>(sb + b * 64 * kRowBytes, &maps.b[0],
+                                                     p.col0 + b0 + b * 64, p.row0 + k, bar);
+                        } else if (boxes > 0) {
+                            if constexpr (C::kRows)
+                                tc::tma_3d<CTAS>(sb, &maps.b[boxes - 1], k, p.col0 + b0, p.e, bar);
+                            else
+                                tc::tma_2d<CTAS>(sb, &maps.b[boxes - 1], k, p.row0 + b0, bar);
                         }
                     }
                     if (!ok) break;
@@ -869,7 +881,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap amap,
                             fence_proxy_async();
                             __syncwarp();
                             if (lane == 0)
-                                tc::tma_store_3d(&omap, stage_out,
+                                tc::tma_store_3d(&maps.out, stage_out,
                                                  p.col0 + c0 + g * 32 / per * per, p.m0 + q * 32,
                                                  p.e, a.accumulate);
                         }
@@ -972,43 +984,65 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 enum Type { kBytes, kBf16, kF32 };
 
-// [outer][rows][inner] elements (outer 0: two dimensions), boxes of 128 bytes x
-// box_rows with the 128-byte swizzle; what lies outside reads as zero.
-bool encode(CUtensorMap* m, Type type, const void* base, int inner, int64_t rows, int outer,
-            int box_rows) {
+// A tensor map of `rank` dimensions (strides of all but the first, in bytes),
+// boxes with the 128-byte swizzle; what lies outside reads as zero.
+bool encode(CUtensorMap* m, Type type, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
-    const uint64_t size = type == kBytes ? 1 : type == kBf16 ? 2 : 4;
-    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
-    const cuuint64_t strides[2] = {inner * size, inner * size * (uint64_t)rows};
-    const cuuint32_t box[3] = {(cuuint32_t)(kRowBytes / size), (cuuint32_t)box_rows, 1};
-    const cuuint32_t es[3] = {1, 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
     const CUtensorMapDataType dt = type == kBytes  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : type == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    return enc(m, dt, outer > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
+    return enc(m, dt, rank, const_cast<void*>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [outer][rows][inner] (outer 0: two dimensions), boxes of 128 bytes x box_rows.
+bool encode_rows(CUtensorMap* m, Type type, const void* base, int inner, int64_t rows, int outer,
+                 int box_rows) {
+    const cuuint64_t size = type == kBytes ? 1 : type == kBf16 ? 2 : 4;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
+    const cuuint64_t strides[2] = {inner * size, inner * size * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {(cuuint32_t)(kRowBytes / size), (cuuint32_t)box_rows, 1};
+    return encode(m, type, base, outer > 0 ? 3 : 2, dims, strides, box);
+}
+
+// The same bf16 array with its rows as runs of 64 columns, [outer][run][rows][64]:
+// boxes of 64 rows of two runs, one behind the other.
+bool encode_runs(CUtensorMap* m, const void* base, int inner, int64_t rows, int outer) {
+    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)inner / 64, (cuuint64_t)outer};
+    const cuuint64_t strides[3] = {(cuuint64_t)inner * 2, 128,
+                                   (cuuint64_t)inner * 2 * (cuuint64_t)rows};
+    const cuuint32_t box[4] = {64, 64, 2, 1};
+    return encode(m, kBf16, base, outer > 0 ? 4 : 3, dims, strides, box);
+}
+
 template <int MODE, bool FP8, int BN, int CTAS>
-coli_status launch_mm(const void* A, const void* B, const MmArgs& a, int N, int K, cudaStream_t st) {
+coli_status launch_mm(const void* A, const void* B, MmArgs a, int N, int K, cudaStream_t st) {
     using C = Cfg<MODE, FP8, BN, CTAS>;
     const Type in = FP8 ? kBytes : kBf16;
-    CUtensorMap amap, bmap, big, omap;
+    Maps maps = {};
     bool ok;
     if constexpr (MODE == kDw) {
-        ok = encode(&amap, in, A, N, a.R, 0, 64) && encode(&bmap, in, B, K, a.R, 0, 64) &&
-             encode(&omap, a.out_bf16 ? kBf16 : kF32, a.out, K, N, a.E, 32);
-        big = bmap;  // not used
-    } else if constexpr (C::kRows) {
-        ok = encode(&amap, in, A, K, a.R, 0, kBM) && encode(&bmap, in, B, K, N, a.E, C::kBoxRows);
-        big = omap = bmap;  // not used
+        a.a_wide = N % 64 == 0;
+        a.b_wide = K % 64 == 0;
+        ok = encode_rows(&maps.a[0], in, A, N, a.R, 0, 64) &&
+             encode_rows(&maps.b[0], in, B, K, a.R, 0, 64) &&
+             (!a.a_wide || encode_runs(&maps.a[1], A, N, a.R, 0)) &&
+             (!a.b_wide || encode_runs(&maps.b[1], B, K, a.R, 0)) &&
+             encode_rows(&maps.out, a.out_bf16 ? kBf16 : kF32, a.out, K, N, a.E, 32);
     } else {
-        ok = encode(&amap, in, A, K, N, a.E, MODE == kFwd ? kBM : 64) &&
-             encode(&bmap, in, B, MODE == kFwd ? K : N, a.R, 0, C::kBoxRows) &&
-             encode(&big, in, B, MODE == kFwd ? K : N, a.R, 0, C::kBigBox);
-        omap = amap;  // not used
+        a.a_wide = MODE == kDx && K % 64 == 0;
+        if constexpr (C::kRows)
+            ok = encode_rows(&maps.a[0], in, A, K, a.R, 0, kBM);
+        else
+            ok = encode_rows(&maps.a[0], in, A, K, N, a.E, MODE == kFwd ? kBM : 64) &&
+                 (!a.a_wide || encode_runs(&maps.a[1], A, K, N, a.E));
+        for (int i = 0; i < C::kBoxes && ok; ++i)
+            ok = encode_rows(&maps.b[i], in, B, MODE == kDx ? N : K, C::kRows ? N : a.R,
+                             C::kRows ? a.E : 0, (i + 1) * C::kBoxRows);
     }
     if (!ok) return COLI_ERR_CUDA;
     int dev = 0, sms = 0;
@@ -1036,7 +1070,7 @@ coli_status launch_mm(const void* A, const void* B, const MmArgs& a, int N, int 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CTAS == 2 ? 2 : 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, amap, bmap, big, omap, a);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, maps, a);
     return err == cudaSuccess ? COLI_OK : COLI_ERR_CUDA;
 }
 
