@@ -55,16 +55,16 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 // Arrive on `bar` when the MMAs issued so far are done; with CTAS = 2 on the
 // barrier at the same place in both CTAs of the pair.
 template <int CTAS>
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint32_t bar) {
     if constexpr (CTAS == 1)
         asm volatile(
             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                smem_addr(bar))
+                bar)
             : "memory");
     else
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
-            ".b64 [%0], %1;" ::"r"(smem_addr(bar)),
+            ".b64 [%0], %1;" ::"r"(bar),
             "h"((uint16_t)3)
             : "memory");
 }
@@ -124,50 +124,50 @@ __device__ __forceinline__ void ld_wait(uint32_t (&v)[16]) {
 // ---- tensor-map loads; `bar` is a shared::cluster address.  With CTAS = 2 the
 // barrier may be the pair's other CTA's. ----
 template <int CTAS>
-__device__ __forceinline__ void tma_2d(void* dst, const void* map, int c0, int c1, uint32_t bar) {
+__device__ __forceinline__ void tma_2d(uint32_t dst, const void* map, int c0, int c1, uint32_t bar) {
     if constexpr (CTAS == 1)
         asm volatile(
             "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
             "l"(map), "r"(c0), "r"(c1), "r"(bar)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global"
-            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
             "l"(map), "r"(c0), "r"(c1), "r"(bar)
             : "memory");
 }
 template <int CTAS>
-__device__ __forceinline__ void tma_3d(void* dst, const void* map, int c0, int c1, int c2,
+__device__ __forceinline__ void tma_3d(uint32_t dst, const void* map, int c0, int c1, int c2,
                                        uint32_t bar) {
     if constexpr (CTAS == 1)
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
             "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global"
-            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
             "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
             : "memory");
 }
 
 template <int CTAS>
-__device__ __forceinline__ void tma_4d(void* dst, const void* map, int c0, int c1, int c2, int c3,
+__device__ __forceinline__ void tma_4d(uint32_t dst, const void* map, int c0, int c1, int c2, int c3,
                                        uint32_t bar) {
     if constexpr (CTAS == 1)
         asm volatile(
             "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+            "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
             "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global"
-            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
             "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
             : "memory");
 }
@@ -215,6 +215,13 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
 // Arrive on a barrier of the cluster; the second form also releases this
 // thread's writes to the other CTA (it waits for them, the first does not).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
@@ -228,19 +235,34 @@ __device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
 // after many tries (each of which may itself suspend the thread for a while):
 // on the path of a pipeline that is waited for at every step, reading it at
 // the first miss costs more than the wait.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+    if (try_wait(bar, parity)) return true;
     uint64_t t0 = 0;
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (try_wait(bar, parity)) return true;
         const uint64_t t = global_timer_ns();
         if (t0 == 0) t0 = t;
         else if (t - t0 > kWaitLimitNs) return false;
     }
 }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    return wait(smem_addr(bar), parity);
+}
 // The same, and acquires what another CTA of the cluster released.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
     for (;;) {
 #pragma unroll 1
@@ -251,7 +273,7 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
                 "selp.u32 %0, 1, 0, p;\n\t}"
                 : "=r"(ok)
-                : "r"(smem_addr(bar)), "r"(parity)
+                : "r"(bar), "r"(parity)
                 : "memory");
             if (ok) return true;
         }
