@@ -65,7 +65,8 @@ constexpr int kSmemMax = 227 * 1024;
 // range: partial sums take about 5 us to leave and be added up, a K-block 0.4.
 constexpr int kMinRange = 12, kCutCost = 12;
 constexpr int kBand = 8;
-constexpr int kStoreBytes = 32 * 128;  // kDw: staging of one warp's stores
+// kDw: a warp's stores leave through kStoreBufs stagings of 32 rows x 64 bytes
+constexpr int kStoreBytes = 32 * 64, kStoreBufs = 3;
 
 // Tensor maps of a call.  An MN-major operand is copied 64 columns at a time
 // (a[0], b[0]), or 128 at once where its rows are whole runs of 64 columns
@@ -118,10 +119,10 @@ struct Cfg {
     // warpgroup gives registers to the epilogue's two.
     static constexpr int kFront = 4;
     static constexpr bool kSplitRegs = kAcc > 64;
-    static constexpr int kFrontRegs = kRows ? 56 : 72, kEpiRegs = kRows ? 224 : 216;
+    static constexpr int kFrontRegs = 72, kEpiRegs = 216;
     static_assert(128 * kFrontRegs + 256 * kEpiRegs <= 384 * 168, "register split");
     static constexpr int kThreads = (kFront + kEpiWarps) * 32;
-    static constexpr int kStoreStage = MODE == kDw ? kEpiWarps * kStoreBytes : 0;
+    static constexpr int kStoreStage = MODE == kDw ? kEpiWarps * kStoreBufs * kStoreBytes : 0;
     static constexpr int kScaleBytes =
         kColScale ? kScaleBufs * BN * 4 : kRows && FP8 ? kScaleRing * kEpiWarps * 32 * 8 : 0;
 };
@@ -720,17 +721,16 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
         if constexpr (C::kSplitRegs) tc::regs_inc<C::kEpiRegs>();
         const int q = warp & 3, half = (warp - C::kFront) >> 2;
         const int mrow = q * 32 + lane;       // row of this CTA's part of the tile
-        uint8_t* stage_out = store0 + (warp - C::kFront) * kStoreBytes;
+        uint8_t* stage_out = store0 + (warp - C::kFront) * kStoreBufs * kStoreBytes;
+        int store_buf = 0;
         const uint32_t acc_empty[2] = {
             CTAS == 2 ? tc::cluster_addr(&s.acc_empty[0], 0) : smem_addr(&s.acc_empty[0]),
             CTAS == 2 ? tc::cluster_addr(&s.acc_empty[1], 0) : smem_addr(&s.acc_empty[1])};
         uint32_t ch = 0;
         while (!*abort && walk.next(p)) {
             // the two warps of a lane quarter share the columns evenly
-            // (kDw: in whole stores of 64 bf16 values; kFwdRows: the columns of one
-            // weight scale each)
-            constexpr int kShare = MODE == kDw ? 64 : 32;
-            const int hn = C::kRows ? 128 : (p.n + 2 * kShare - 1) / (2 * kShare) * kShare;
+            // (kFwdRows: the columns of one weight scale each)
+            const int hn = C::kRows ? 128 : (p.n + 63) / 64 * 32;
             const int c0 = half * hn;                       // first column of this thread
             const int nc = max(0, min(p.n - c0, hn));       // and how many
             const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
@@ -767,6 +767,14 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                 const int n_ch = (p.kb1 - p.kb0 + len - 1) / len;
                 for (int i = 0; i < n_ch; ++i, ++ch) {
                     const uint32_t buf = ch & 1, sb = ch % kScaleBufs;
+                    // what does not need the accumulator stays out of the way from
+                    // one accumulator's MMAs over its drain to the next one's
+                    float one = 0.f;
+                    if constexpr (C::kRows) {
+                        tc::cp_async_wait<kScaleRing - 2>();
+                        const float2 f = ring[(i & (kScaleRing - 1)) * (kEpiWarps * 32)];
+                        one = f.x * f.y;
+                    }
                     if (!tc::wait(&s.acc_full[buf], (ch / 2) & 1) ||
                         (C::kColScale && !tc::wait(&s.sc_full[sb], (ch / kScaleBufs) & 1))) {
                         if (lane == 0) timeout();
@@ -776,13 +784,6 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     tc::fence_after();
                     const uint32_t src = tq + buf * C::BN;
                     const float* sc = scale0 + sb * C::BN + c0;
-                    float one = 0.f;
-                    if constexpr (C::kRows) {
-                        tc::cp_async_wait<kScaleRing - 2>();
-                        const float2 f = ring[(i & (kScaleRing - 1)) * (kEpiWarps * 32)];
-                        one = f.x * f.y;
-                        fetch(i + kScaleRing - 1);
-                    }
                     auto release = [&]() {
                         tc::fence_before();
                         __syncwarp();
@@ -795,6 +796,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     if (nc == C::kAcc) drain<C, FP8, true>(src, sc, one, nc, acc, release);
                     else if (nc > 0) drain<C, FP8, false>(src, sc, one, nc, acc, release);
                     else release();
+                    if constexpr (C::kRows) fetch(i + kScaleRing - 1);
                 }
             }
             if (!ok) break;
@@ -853,49 +855,48 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
 
             const int m = p.m0 + mrow;
             if constexpr (MODE == kDw) {
-                // 32 rows x 128 bytes at a time through shared memory to a tensor
-                // store, which leaves out what lies outside dw
+                // 32 rows x 64 bytes at a time through shared memory to a tensor
+                // store, which leaves out what lies outside dw; up to kStoreBufs of
+                // them under way
                 if (!(a.accumulate && a.out_bf16)) {
-                    const int per = a.out_bf16 ? 64 : 32;   // columns per store
 #pragma unroll
-                    for (int g = 0; g < C::kAcc / 32; ++g) {
-                        if (g * 32 >= nc || p.m0 + q * 32 >= a.M) break;
-                        // bf16: two groups of 32 columns fill one store
-                        if (!a.out_bf16 || (g & 1) == 0) {
-                            if (lane == 0) tc::store_read_wait();
-                            __syncwarp();
-                        }
+                    for (int g = 0; g < C::kAcc / 16; ++g) {
+                        // 16 fp32 columns, or 32 bf16 ones of every other group
+                        if (g * 16 >= nc || p.m0 + q * 32 >= a.M) break;
+                        if (a.out_bf16 && (g & 1)) continue;
+                        uint8_t* out = stage_out + store_buf * kStoreBytes;
+                        store_buf = store_buf + 1 == kStoreBufs ? 0 : store_buf + 1;
+                        if (lane == 0) tc::store_read_wait<kStoreBufs - 1>();
+                        __syncwarp();
+                        // 64-byte swizzle: rows in pairs of 128 bytes
+                        uint8_t* row = out + lane * 64;
+                        const int x = (lane >> 1) & 3;
                         if (a.out_bf16) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 uint32_t u[4];
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    const float* f = acc + g * 32 + 8 * j + 2 * i;
+                                    constexpr int kLast = C::kAcc - 2;
+                                    const float* f = acc + min(g * 16 + 8 * j + 2 * i, kLast);
                                     const __nv_bfloat162 h = __floats2bfloat162_rn(f[0], f[1]);
                                     u[i] = *reinterpret_cast<const uint32_t*>(&h);
                                 }
-                                const int chunk = (g & 1) * 4 + j;
-                                *reinterpret_cast<uint4*>(stage_out + lane * 128 +
-                                                          ((chunk ^ (lane & 7)) << 4)) =
+                                *reinterpret_cast<uint4*>(row + ((j ^ x) << 4)) =
                                     make_uint4(u[0], u[1], u[2], u[3]);
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                *reinterpret_cast<float4*>(stage_out + lane * 128 +
-                                                           ((j ^ (lane & 7)) << 4)) =
-                                    make_float4(acc[g * 32 + 4 * j], acc[g * 32 + 4 * j + 1],
-                                                acc[g * 32 + 4 * j + 2], acc[g * 32 + 4 * j + 3]);
+                            for (int j = 0; j < 4; ++j)
+                                *reinterpret_cast<float4*>(row + ((j ^ x) << 4)) =
+                                    make_float4(acc[g * 16 + 4 * j], acc[g * 16 + 4 * j + 1],
+                                                acc[g * 16 + 4 * j + 2], acc[g * 16 + 4 * j + 3]);
                         }
-                        if (!a.out_bf16 || (g & 1) || (g + 1) * 32 >= nc) {
-                            fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0)
-                                tc::tma_store_3d(&maps.out, stage_out,
-                                                 p.col0 + c0 + g * 32 / per * per, p.m0 + q * 32,
-                                                 p.e, a.accumulate);
-                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::tma_store_3d(&maps.out, out, p.col0 + c0 + g * 16, p.m0 + q * 32,
+                                             p.e, a.accumulate);
                     }
                 } else if (m < a.M) {
                     // added to bf16 values: one rounding of the whole sum
@@ -996,9 +997,11 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 enum Type { kBytes, kBf16, kF32 };
 
 // A tensor map of `rank` dimensions (strides of all but the first, in bytes),
-// boxes with the 128-byte swizzle; what lies outside reads as zero.
+// boxes with the 128-byte swizzle (or the 64-byte one, for boxes that wide); what
+// lies outside reads as zero.
 bool encode(CUtensorMap* m, Type type, const void* base, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box) {
+            const cuuint64_t* strides, const cuuint32_t* box,
+            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint32_t es[4] = {1, 1, 1, 1};
@@ -1006,18 +1009,20 @@ bool encode(CUtensorMap* m, Type type, const void* base, int rank, const cuuint6
                                    : type == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     return enc(m, dt, rank, const_cast<void*>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [outer][rows][inner] (outer 0: two dimensions), boxes of 128 bytes x box_rows.
+// [outer][rows][inner] (outer 0: two dimensions), boxes of 128 (or 64) bytes x
+// box_rows.
 bool encode_rows(CUtensorMap* m, Type type, const void* base, int inner, int64_t rows, int outer,
-                 int box_rows) {
+                 int box_rows, int box_bytes = kRowBytes) {
     const cuuint64_t size = type == kBytes ? 1 : type == kBf16 ? 2 : 4;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
     const cuuint64_t strides[2] = {inner * size, inner * size * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {(cuuint32_t)(kRowBytes / size), (cuuint32_t)box_rows, 1};
-    return encode(m, type, base, outer > 0 ? 3 : 2, dims, strides, box);
+    const cuuint32_t box[3] = {(cuuint32_t)(box_bytes / size), (cuuint32_t)box_rows, 1};
+    return encode(m, type, base, outer > 0 ? 3 : 2, dims, strides, box,
+                  box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // The same bf16 array with its rows as runs of 64 columns, [outer][run][rows][64]:
@@ -1043,7 +1048,7 @@ coli_status launch_mm(const void* A, const void* B, MmArgs a, int N, int K, cuda
              encode_rows(&maps.b[0], in, B, K, a.R, 0, 64) &&
              (!a.a_wide || encode_runs(&maps.a[1], A, N, a.R, 0)) &&
              (!a.b_wide || encode_runs(&maps.b[1], B, K, a.R, 0)) &&
-             encode_rows(&maps.out, a.out_bf16 ? kBf16 : kF32, a.out, K, N, a.E, 32);
+             encode_rows(&maps.out, a.out_bf16 ? kBf16 : kF32, a.out, K, N, a.E, 32, 64);
     } else {
         a.a_wide = MODE == kDx && K % 64 == 0;
         if constexpr (C::kRows)
