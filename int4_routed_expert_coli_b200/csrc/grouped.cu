@@ -21,8 +21,8 @@
 //     the tensor cores' fp32 accumulation truncates, and a chain of 6144
 //     products is 7e-6 off (16384: 2e-5), one of 768 below 1e-6;
 //   * an e4m3 sum is drained every block of 128, times the block's two scales
-//     (the row's and the weight block's, whose product warps 2 and 3 put in
-//     shared memory: a weight tile's 128 rows are one scale block).
+//     (the row's and the weight block's; a tile's 128 weight rows are one scale
+//     block), which are copied ahead into shared memory.
 //
 // Tiles: whole waves of tiles are dealt to the CTAs in order; the tiles of the
 // last, incomplete wave are dealt as one sequence of K-blocks, cut into equal
@@ -54,10 +54,12 @@ constexpr int kBM = 128;               // M per CTA
 constexpr int kRowBytes = 128;         // bytes of one operand row (or column) per stage
 constexpr int kABytes = kBM * kRowBytes;
 constexpr int kMaxStages = 12;
+constexpr int kTmemAll = 512;          // tensor memory columns
+constexpr int kMaxBufs = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kMaxGrid = 148;
 constexpr int kChunk = 12;             // bf16 K-blocks per accumulator chain, at most
-constexpr int kScaleBufs = 4;
+constexpr int kScaleBufs = 8;
 constexpr int kScaleRing = 8;          // kFwdRows: K-blocks whose scales are loaded ahead
 constexpr int kSmemMax = 227 * 1024;
 // The last wave is cut into ranges of kMinRange K-blocks at least, and not at
@@ -107,13 +109,13 @@ struct Cfg {
     static constexpr int kBoxes = MODE == kDw ? 0 : BN / CTAS / kBoxRows;
     static constexpr int kBBytes = BN / CTAS * kRowBytes;
     static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kTmemCols = 2 * BN;
+    static constexpr int kBufs = kTmemAll / BN;            // accumulators
     static constexpr int kNGrain = 16 * CTAS;              // MMA N in multiples of this
     static constexpr bool kAMn = MODE == kDx || MODE == kDw;
     static constexpr bool kBMn = MODE == kDw;
     static constexpr bool kColScale = FP8 && !kRows;       // scales per column, in shared memory
     static constexpr int kAcc = BN / 2;                    // accumulators per epilogue thread
-    // Four front warps (loads, MMAs, two that multiply scales or clear), eight of
+    // Four front warps (loads, MMAs, one that copies scales or clears), eight of
     // the epilogue.  A wide tile's epilogue thread holds 128 sums and 32 loaded
     // values, more than 384 threads can have each (168 registers): the front
     // warpgroup gives registers to the epilogue's two.
@@ -123,14 +125,15 @@ struct Cfg {
     static_assert(128 * kFrontRegs + 256 * kEpiRegs <= 384 * 168, "register split");
     static constexpr int kThreads = (kFront + kEpiWarps) * 32;
     static constexpr int kStoreStage = MODE == kDw ? kEpiWarps * kStoreBufs * kStoreBytes : 0;
+    static constexpr int kScaleSlot = BN + 4;              // floats (a multiple of 16 bytes)
     static constexpr int kScaleBytes =
-        kColScale ? kScaleBufs * BN * 4 : kRows && FP8 ? kScaleRing * kEpiWarps * 32 * 8 : 0;
+        kColScale ? kScaleBufs * kScaleSlot * 4 : kRows && FP8 ? kScaleRing * kEpiWarps * 32 * 8 : 0;
 };
 
 // Everything of shared memory but the stages.
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t acc_full[kMaxBufs], acc_empty[kMaxBufs];
     uint64_t sc_full[kScaleBufs], sc_empty[kScaleBufs];
     // kDw, a group's cut last K-block: its copies are done; the rows behind the
     // group's end are cleared
@@ -142,6 +145,7 @@ struct Shared {
     int whole, wave, range;                // whole tiles; steps of the last wave, of a range of it
     long long base;                        // first step of the last wave
     long long scan[2][16];
+    int off[kMaxExperts + 1];              // the offsets (checked where a group has tiles)
     int tile0[kMaxExperts + 1];            // first tile (of the first M tile column) of each group
     long long step0[kMaxExperts + 1];      // K-block steps before each group
 };
@@ -188,9 +192,9 @@ struct Walk {
     }
     // rows of a row tile, at most
     static constexpr int kTileRows = C::kRows ? kBM * C::CTAS : C::BN;
-    static __device__ __forceinline__ int group_kb(const MmArgs& a, int e) {
+    static __device__ __forceinline__ int group_kb(const MmArgs& a, const Shared& s, int e) {
         if (MODE != kDw) return (a.red + C::BK - 1) / C::BK;
-        const int rows = __ldg(a.offsets + e + 1) - __ldg(a.offsets + e);
+        const int rows = s.off[e + 1] - s.off[e];
         return max(1, (rows + C::BK - 1) / C::BK);
     }
     // The last group with first[e] * per <= v.
@@ -212,7 +216,7 @@ struct Walk {
         long long base = steps;
         if (full < tiles) {
             const int e = group_of(s.tile0, per, full, a.E);
-            base = s.step0[e] * per + (full - s.tile0[e] * per) * group_kb(a, e);
+            base = s.step0[e] * per + (full - s.tile0[e] * per) * group_kb(a, s, e);
         }
         const int wave = (int)(steps - base);
         const int range = max(kMinRange, (wave + workers() - 1) / workers());
@@ -228,7 +232,7 @@ struct Walk {
         end = min(s.wave, cur + s.range);
     }
     __device__ __forceinline__ void fill(Piece& p, int e, int t, int kb) const {
-        const int off = __ldg(a.offsets + e), rows = __ldg(a.offsets + e + 1) - off;
+        const int off = s.off[e], rows = s.off[e + 1] - off;
         p.e = e;
         p.kb = kb;
         if (MODE == kDw) {
@@ -265,7 +269,7 @@ struct Walk {
     __device__ __forceinline__ bool next(Piece& p) {
         const long long per = (long long)m_tiles(a) * c_tiles(a);
         if (tile < s.whole) {
-            const int e = group_of(s.tile0, per, tile, a.E), kb = group_kb(a, e);
+            const int e = group_of(s.tile0, per, tile, a.E), kb = group_kb(a, s, e);
             fill(p, e, (int)(tile - s.tile0[e] * per), kb);
             p.kb0 = 0;
             p.kb1 = kb;
@@ -275,7 +279,7 @@ struct Walk {
         }
         if (cur >= end) return false;
         const long long at = s.base + cur;
-        const int e = group_of(s.step0, per, at, a.E), kb = group_kb(a, e);
+        const int e = group_of(s.step0, per, at, a.E), kb = group_kb(a, s, e);
         const long long in = at - s.step0[e] * per;
         const int t = (int)(in / kb);
         fill(p, e, t, kb);
@@ -300,8 +304,8 @@ __device__ __forceinline__ int mma_n(int n) {
     return (max(n, 1) + C::kNGrain - 1) / C::kNGrain * C::kNGrain;
 }
 
-// Add one accumulator's columns (times their scales: `sc` per column or `one`
-// for all) to a thread's sums, and call `release` once they are all loaded.
+// Add one accumulator's columns (times their scales: `one` for all, and where
+// there are some `sc` per column) to a thread's sums, and call `release` once they are all loaded.
 // The loads of 16 columns run under the sums of the 16 before; a whole tile's
 // loop has no branches, so its instructions interleave.
 template <class C, bool FP8, bool WHOLE, class Release>
@@ -331,10 +335,10 @@ __device__ __forceinline__ void drain(uint32_t src, const float* sc, float one, 
                 tc::fma2(d, w + 4 * j, one);
                 tc::fma2(d + 2, w + 4 * j + 2, one);
             } else if constexpr (C::kColScale) {
-                d[0] += __uint_as_float(w[4 * j]) * f[j].x;
-                d[1] += __uint_as_float(w[4 * j + 1]) * f[j].y;
-                d[2] += __uint_as_float(w[4 * j + 2]) * f[j].z;
-                d[3] += __uint_as_float(w[4 * j + 3]) * f[j].w;
+                d[0] += __uint_as_float(w[4 * j]) * (f[j].x * one);
+                d[1] += __uint_as_float(w[4 * j + 1]) * (f[j].y * one);
+                d[2] += __uint_as_float(w[4 * j + 2]) * (f[j].z * one);
+                d[3] += __uint_as_float(w[4 * j + 3]) * (f[j].w * one);
             } else {
                 d[0] += __uint_as_float(w[4 * j]);
                 d[1] += __uint_as_float(w[4 * j + 1]);
@@ -368,19 +372,19 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
             mbar_init(&s.tail_full[i], 1);
             mbar_init(&s.tail_ready[i], CTAS);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kBufs; ++i) {
             mbar_init(&s.acc_full[i], 1);
             mbar_init(&s.acc_empty[i], kEpiWarps * CTAS);
         }
         for (int i = 0; i < kScaleBufs; ++i) {
-            mbar_init(&s.sc_full[i], 1);
+            mbar_init(&s.sc_full[i], 32);  // one arrival per copying lane
             mbar_init(&s.sc_empty[i], kEpiWarps);
         }
         s.abort = 0;
         s.kb_max = MODE == kDw ? 0 : (a.red + C::BK - 1) / C::BK;
         fence_barrier_init();
     }
-    if (warp == 1) tc::alloc<CTAS>(&s.tmem, C::kTmemCols);
+    if (warp == 1) tc::alloc<CTAS>(&s.tmem, kTmemAll);
     if (threadIdx.x == 0) {
         tc::prefetch_map(&maps.a[0]);
         tc::prefetch_map(&maps.b[0]);
@@ -401,6 +405,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
             v[i] = w[i] = 0;
             if (e < a.E) {
                 const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
+                s.off[e] = lo;
+                if (e + 1 == a.E) s.off[e + 1] = hi;
                 if (lo < 0 || hi < lo || hi > a.R) {
                     report(a.status, COLI_ERR_BAD_INDEX);
                 } else if (MODE == kDw) {
@@ -638,8 +644,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                             }
                         }
                         tc::commit<CTAS>(afull0 + buf * 8);
-                        buf ^= 1;
-                        drained ^= buf ^ 1;
+                        buf = buf + 1 == C::kBufs ? 0 : buf + 1;
+                        drained ^= buf == 0;
                         if (!looked) {
                             more = walk.next(nxt);
                             looked = true;
@@ -685,35 +691,36 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                 }
             }
         } else if constexpr (C::kColScale) {
-            // ------------- fp8: products of the two scales, per column --------------
-            const int KB = (a.red + C::BK - 1) / C::BK;
-            const int w_tiles = (a.M + kBM - 1) / kBM;
-            uint32_t ch = 0;
-            while (!*abort && walk.next(p)) {
-                // (an odd CTA past the last weight rows computes nothing that is stored)
-                const int wt = min(p.m0 / kBM, w_tiles - 1);
-                const float* wsc = a.ws + ((int64_t)p.e * w_tiles + wt) * KB;
-                bool ok = true;
-                for (int kb = p.kb0; kb < p.kb1; ++kb, ++ch) {
-                    if ((int)(ch & 1) != warp - 2) continue;  // the two warps alternate
-                    const int b = ch % kScaleBufs;
-                    const float sw = __ldg(wsc + kb);
-                    const float* xs = a.xs + (int64_t)kb * a.R + p.row0;
-                    float v[C::BN / 32];
+            // ----------- fp8: the rows' scales (one per column) and the weights' ----------
+            // Copied ahead (cp.async) into a ring of kScaleBufs K-blocks; a slot holds
+            // the columns' scales and, behind them, the weights' scale.
+            if (warp == 2) {
+                const int KB = (a.red + C::BK - 1) / C::BK;
+                const int w_tiles = (a.M + kBM - 1) / kBM;
+                uint32_t ch = 0;
+                while (!*abort && walk.next(p)) {
+                    // (an odd CTA past the last weight rows computes nothing that is stored)
+                    const int wt = min(p.m0 / kBM, w_tiles - 1);
+                    const float* wsc = a.ws + ((int64_t)p.e * w_tiles + wt) * KB + p.kb0;
+                    const float* xs = a.xs + (int64_t)p.kb0 * a.R + p.row0;
+                    bool ok = true;
+                    for (int kb = p.kb0; kb < p.kb1; ++kb, ++ch, ++wsc, xs += a.R) {
+                        const uint32_t b = ch % kScaleBufs;
+                        if (!tc::wait(&s.sc_empty[b], (ch / kScaleBufs & 1) ^ 1)) {
+                            if (lane == 0) timeout();
+                            ok = false;
+                            break;
+                        }
+                        float* slot = scale0 + b * C::kScaleSlot;
 #pragma unroll
-                    for (int j = 0; j < C::BN / 32; ++j)
-                        v[j] = j * 32 + lane < p.n ? __ldg(xs + j * 32 + lane) * sw : 0.f;
-                    if (ch >= kScaleBufs && !tc::wait(&s.sc_empty[b], (ch / kScaleBufs - 1) & 1)) {
-                        if (lane == 0) timeout();
-                        ok = false;
-                        break;
+                        for (int j = lane; j < C::BN; j += 32)
+                            if (j < p.n) cp_async4(slot + j, xs + j);
+                        if (lane == 0) cp_async4(slot + C::BN, wsc);
+                        tc::cp_async_arrive(&s.sc_full[b]);
                     }
-#pragma unroll
-                    for (int j = 0; j < C::BN / 32; ++j) scale0[b * C::BN + j * 32 + lane] = v[j];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.sc_full[b]);
+                    if (!ok) break;
                 }
-                if (!ok) break;
+                tc::cp_async_wait<0>();
             }
         }
     } else {
@@ -723,9 +730,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
         const int mrow = q * 32 + lane;       // row of this CTA's part of the tile
         uint8_t* stage_out = store0 + (warp - C::kFront) * kStoreBufs * kStoreBytes;
         int store_buf = 0;
-        const uint32_t acc_empty[2] = {
-            CTAS == 2 ? tc::cluster_addr(&s.acc_empty[0], 0) : smem_addr(&s.acc_empty[0]),
-            CTAS == 2 ? tc::cluster_addr(&s.acc_empty[1], 0) : smem_addr(&s.acc_empty[1])};
+        const uint32_t acc_empty =
+            CTAS == 2 ? tc::cluster_addr(&s.acc_empty[0], 0) : smem_addr(&s.acc_empty[0]);
         uint32_t ch = 0;
         while (!*abort && walk.next(p)) {
             // the two warps of a lane quarter share the columns evenly
@@ -766,7 +772,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                 const int len = chain_len<FP8>(p.kb1 - p.kb0);
                 const int n_ch = (p.kb1 - p.kb0 + len - 1) / len;
                 for (int i = 0; i < n_ch; ++i, ++ch) {
-                    const uint32_t buf = ch & 1, sb = ch % kScaleBufs;
+                    const uint32_t buf = ch % C::kBufs, sb = ch % kScaleBufs;
                     // what does not need the accumulator stays out of the way from
                     // one accumulator's MMAs over its drain to the next one's
                     float one = 0.f;
@@ -775,7 +781,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                         const float2 f = ring[(i & (kScaleRing - 1)) * (kEpiWarps * 32)];
                         one = f.x * f.y;
                     }
-                    if (!tc::wait(&s.acc_full[buf], (ch / 2) & 1) ||
+                    if (!tc::wait(&s.acc_full[buf], (ch / C::kBufs) & 1) ||
                         (C::kColScale && !tc::wait(&s.sc_full[sb], (ch / kScaleBufs) & 1))) {
                         if (lane == 0) timeout();
                         ok = false;
@@ -783,18 +789,19 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     }
                     tc::fence_after();
                     const uint32_t src = tq + buf * C::BN;
-                    const float* sc = scale0 + sb * C::BN + c0;
+                    const float* sc = scale0 + sb * C::kScaleSlot;
+                    if constexpr (C::kColScale) one = sc[C::BN];
                     auto release = [&]() {
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            if (CTAS == 2) tc::arrive_cluster(acc_empty[buf]);
-                            else mbar_arrive(&s.acc_empty[buf]);
+                            if (CTAS == 2) tc::arrive_cluster(acc_empty + buf * 8);
+                            else tc::arrive(acc_empty + buf * 8);
                             if (C::kColScale) mbar_arrive(&s.sc_empty[sb]);
                         }
                     };
-                    if (nc == C::kAcc) drain<C, FP8, true>(src, sc, one, nc, acc, release);
-                    else if (nc > 0) drain<C, FP8, false>(src, sc, one, nc, acc, release);
+                    if (nc == C::kAcc) drain<C, FP8, true>(src, sc + c0, one, nc, acc, release);
+                    else if (nc > 0) drain<C, FP8, false>(src, sc + c0, one, nc, acc, release);
                     else release();
                     if constexpr (C::kRows) fetch(i + kScaleRing - 1);
                 }
@@ -974,7 +981,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
     if constexpr (CTAS == 2) tc::cluster_sync();
     if (warp == 1) {
         tc::fence_after();
-        tc::dealloc<CTAS>(tmem, C::kTmemCols);
+        tc::dealloc<CTAS>(tmem, kTmemAll);
     }
 }
 

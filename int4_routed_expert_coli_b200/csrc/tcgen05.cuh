@@ -175,7 +175,8 @@ __device__ __forceinline__ void prefetch_map(const void* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// ---- tensor-map stores (parts outside the tensor are not written) ----
+// ---- tensor-map stores (parts outside the tensor are not written).  What they
+// write leaves L2 first: large results would push the operands out. ----
 __device__ __forceinline__ void tma_store_3d(const void* map, const void* src, int c0, int c1,
                                              int c2, bool add) {
     if (add)
@@ -186,9 +187,9 @@ __device__ __forceinline__ void tma_store_3d(const void* map, const void* src, i
             : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group "
-            "[%0, {%1, %2, %3}], [%4];" ::"l"(map),
-            "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(src))
+            "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint "
+            "[%0, {%1, %2, %3}], [%4], %5;" ::"l"(map),
+            "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(src)), "l"(policy_evict_first())
             : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -294,6 +295,12 @@ __device__ __forceinline__ void fma2(float* d, const uint32_t* v, float s) {
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Arrive on `bar` when this thread's cp.async copies so far are done.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
 }
 
 // ---- register split between warpgroups ----
