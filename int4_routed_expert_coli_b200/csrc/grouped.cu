@@ -59,7 +59,7 @@ constexpr int kMaxBufs = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kMaxGrid = 148;
 constexpr int kChunk = 12;             // bf16 K-blocks per accumulator chain, at most
-constexpr int kScaleBufs = 8;
+constexpr int kScaleBufs = 4;          // handovers whose column scales are loaded ahead
 constexpr int kScaleRing = 8;          // kFwdRows: K-blocks whose scales are loaded ahead
 constexpr int kSmemMax = 227 * 1024;
 // The last wave is cut into ranges of kMinRange K-blocks at least, and not at
@@ -109,11 +109,15 @@ struct Cfg {
     static constexpr int kBoxes = MODE == kDw ? 0 : BN / CTAS / kBoxRows;
     static constexpr int kBBytes = BN / CTAS * kRowBytes;
     static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kBufs = kTmemAll / BN;            // accumulators
+    static constexpr bool kColScale = FP8 && MODE != kFwdRows;  // scales per column
+    // Accumulators per handover: a narrow e4m3 tile's K-block is little work, and
+    // the round trip of its accumulator, paid for each, took 0.53 us of a K-block
+    // whose weights come in 0.2.
+    static constexpr int kBatch = kColScale ? 4 : 1;
+    static constexpr int kBufs = kTmemAll / (BN * kBatch);      // handovers under way
     static constexpr int kNGrain = 16 * CTAS;              // MMA N in multiples of this
     static constexpr bool kAMn = MODE == kDx || MODE == kDw;
     static constexpr bool kBMn = MODE == kDw;
-    static constexpr bool kColScale = FP8 && !kRows;       // scales per column, in shared memory
     static constexpr int kAcc = BN / 2;                    // accumulators per epilogue thread
     // Four front warps (loads, MMAs, one that copies scales or clears), eight of
     // the epilogue.  A wide tile's epilogue thread holds 128 sums and 32 loaded
@@ -127,7 +131,7 @@ struct Cfg {
     static constexpr int kStoreStage = MODE == kDw ? kEpiWarps * kStoreBufs * kStoreBytes : 0;
     static constexpr int kScaleSlot = BN + 4;              // floats (a multiple of 16 bytes)
     static constexpr int kScaleBytes =
-        kColScale ? kScaleBufs * kScaleSlot * 4 : kRows && FP8 ? kScaleRing * kEpiWarps * 32 * 8 : 0;
+        kColScale ? kScaleBufs * kBatch * kScaleSlot * 4 : kRows && FP8 ? kScaleRing * kEpiWarps * 32 * 8 : 0;
 };
 
 // Everything of shared memory but the stages.
@@ -291,12 +295,16 @@ struct Walk {
     }
 };
 
-// Accumulator chains of n K-blocks: as few as possible, of equal lengths (a
-// short one behind a long one would leave the drain no time).
-template <bool FP8>
-__device__ __forceinline__ int chains(int n) { return FP8 ? n : (n + kChunk - 1) / kChunk; }
-template <bool FP8>
-__device__ __forceinline__ int chain_len(int n) { return (n + chains<FP8>(n) - 1) / chains<FP8>(n); }
+// K-blocks of one handover from the MMAs to the epilogue, of n.  bf16: one
+// accumulator chain, as few as possible and of equal lengths (a short one behind
+// a long one would leave the drain no time).  e4m3: kBatch K-blocks, each with
+// its own accumulator.
+template <class C, bool FP8>
+__device__ __forceinline__ int chain_len(int n) {
+    if (FP8) return C::kBatch;
+    const int chains = (n + kChunk - 1) / kChunk;
+    return (n + chains - 1) / chains;
+}
 
 // Columns of the MMA: the valid ones rounded up to its grain.
 template <class C>
@@ -610,13 +618,14 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     }
                     const uint32_t id =
                         tc::idesc(kBM * CTAS, mma_n<C>(p.n), FP8 ? 0 : 1, C::kAMn, C::kBMn);
-                    const int len = chain_len<FP8>(p.kb1 - p.kb0);
+                    const int len = chain_len<C, FP8>(p.kb1 - p.kb0);
                     bool ok = true;
                     for (int c0 = p.kb0; c0 < p.kb1 && ok; c0 += len) {
                         const int c1 = min(c0 + len, p.kb1);
                         ok = tc::wait(aempty0 + buf * 8, drained);
-                        const uint32_t d = tmem + buf * C::BN;
                         for (int kb = c0; kb < c1 && ok; ++kb) {
+                            const uint32_t d =
+                                tmem + (buf * C::kBatch + (C::kBatch > 1 ? kb - c0 : 0)) * C::BN;
                             ok = tc::wait(full0 + stage * 8, full);
                             const uint64_t ad = ad0 + stage * (C::kStage / 16);
                             const uint64_t bd = bd0 + stage * (C::kStage / 16);
@@ -632,7 +641,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                                                        kb > c0 || k > 0);
                             } else if (ok) {
                                 tc::fence_after();
-                                tc::mma<FP8, CTAS>(d, ad, bd, id, kb > c0);
+                                tc::mma<FP8, CTAS>(d, ad, bd, id, !FP8 && kb > c0);
 #pragma unroll
                                 for (int k = 1; k < 4; ++k)
                                     tc::mma<FP8, CTAS>(d, ad + k * kAStep, bd + k * kBStep, id, 1);
@@ -692,8 +701,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
             }
         } else if constexpr (C::kColScale) {
             // ----------- fp8: the rows' scales (one per column) and the weights' ----------
-            // Copied ahead (cp.async) into a ring of kScaleBufs K-blocks; a slot holds
-            // the columns' scales and, behind them, the weights' scale.
+            // Copied ahead (cp.async), kScaleBufs handovers; a K-block's slot holds the
+            // columns' scales and, behind them, the weights' scale.
             if (warp == 2) {
                 const int KB = (a.red + C::BK - 1) / C::BK;
                 const int w_tiles = (a.M + kBM - 1) / kBM;
@@ -704,18 +713,21 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     const float* wsc = a.ws + ((int64_t)p.e * w_tiles + wt) * KB + p.kb0;
                     const float* xs = a.xs + (int64_t)p.kb0 * a.R + p.row0;
                     bool ok = true;
-                    for (int kb = p.kb0; kb < p.kb1; ++kb, ++ch, ++wsc, xs += a.R) {
+                    for (int k0 = p.kb0; k0 < p.kb1; k0 += C::kBatch, ++ch) {
                         const uint32_t b = ch % kScaleBufs;
                         if (!tc::wait(&s.sc_empty[b], (ch / kScaleBufs & 1) ^ 1)) {
                             if (lane == 0) timeout();
                             ok = false;
                             break;
                         }
-                        float* slot = scale0 + b * C::kScaleSlot;
+                        float* slot = scale0 + b * (C::kBatch * C::kScaleSlot);
+                        const int n = min(C::kBatch, p.kb1 - k0);
+                        for (int k = 0; k < n; ++k, ++wsc, xs += a.R, slot += C::kScaleSlot) {
 #pragma unroll
-                        for (int j = lane; j < C::BN; j += 32)
-                            if (j < p.n) cp_async4(slot + j, xs + j);
-                        if (lane == 0) cp_async4(slot + C::BN, wsc);
+                            for (int j = lane; j < C::BN; j += 32)
+                                if (j < p.n) cp_async4(slot + j, xs + j);
+                            if (lane == 0) cp_async4(slot + C::BN, wsc);
+                        }
                         tc::cp_async_arrive(&s.sc_full[b]);
                     }
                     if (!ok) break;
@@ -769,7 +781,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     }
                     for (int i = 0; i < kScaleRing - 1; ++i) fetch(i);
                 }
-                const int len = chain_len<FP8>(p.kb1 - p.kb0);
+                const int len = chain_len<C, FP8>(p.kb1 - p.kb0);
                 const int n_ch = (p.kb1 - p.kb0 + len - 1) / len;
                 for (int i = 0; i < n_ch; ++i, ++ch) {
                     const uint32_t buf = ch % C::kBufs, sb = ch % kScaleBufs;
@@ -788,9 +800,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                         break;
                     }
                     tc::fence_after();
-                    const uint32_t src = tq + buf * C::BN;
-                    const float* sc = scale0 + sb * C::kScaleSlot;
-                    if constexpr (C::kColScale) one = sc[C::BN];
+                    const uint32_t src = tq + buf * (C::kBatch * C::BN);
+                    const float* sc = scale0 + sb * (C::kBatch * C::kScaleSlot);
                     auto release = [&]() {
                         tc::fence_before();
                         __syncwarp();
@@ -800,9 +811,22 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                             if (C::kColScale) mbar_arrive(&s.sc_empty[sb]);
                         }
                     };
-                    if (nc == C::kAcc) drain<C, FP8, true>(src, sc + c0, one, nc, acc, release);
-                    else if (nc > 0) drain<C, FP8, false>(src, sc + c0, one, nc, acc, release);
-                    else release();
+                    if constexpr (C::kColScale) {
+                        const int n = min(C::kBatch, p.kb1 - p.kb0 - i * len);
+                        if (nc > 0) {
+#pragma unroll
+                            for (int k = 0; k < C::kBatch; ++k)
+                                if (k < n)
+                                    drain<C, FP8, false>(src + k * C::BN, sc + k * C::kScaleSlot + c0,
+                                                         sc[k * C::kScaleSlot + C::BN], nc, acc,
+                                                         [] {});
+                        }
+                        release();
+                    } else {
+                        if (nc == C::kAcc) drain<C, FP8, true>(src, sc, one, nc, acc, release);
+                        else if (nc > 0) drain<C, FP8, false>(src, sc, one, nc, acc, release);
+                        else release();
+                    }
                     if constexpr (C::kRows) fetch(i + kScaleRing - 1);
                 }
             }
