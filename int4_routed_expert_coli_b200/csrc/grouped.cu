@@ -1121,9 +1121,12 @@ coli_status launch_mm(const void* A, const void* B, MmArgs a, int N, int K, cuda
     return err == cudaSuccess ? COLI_OK : COLI_ERR_CUDA;
 }
 
-// Narrow row tiles when the groups average at most 32 rows: the loads of the
-// weights bound such calls, and narrow tiles leave room for more of them.
-bool narrow(int R, int E) { return (int64_t)R <= 32 * (int64_t)E; }
+// Narrow row tiles (64 rows, one CTA) where the weights' loads bound the call.
+// Measured at N 4096, K 6144, narrow against wide: one group of 64 rows 28.7 and
+// 34.8 us, of 128 rows 38.9 (narrow 32.8); 32 groups of 32 rows on average 266 and
+// 279 us, of 48 rows 276 and 283, of 64 rows 297 and 285 (e4m3: 156 and 167, 174
+// and 170, 195 and 176).
+bool narrow(int R, int E) { return (int64_t)R <= 48 * (int64_t)E + 16; }
 
 constexpr size_t kPartBytes = sizeof(float) * kMaxGrid * 2 * kBM * 256;
 
