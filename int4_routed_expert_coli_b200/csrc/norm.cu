@@ -19,7 +19,10 @@
 //   a channel gate's dgate = alpha post_w C, a token's = alpha ry sum_h cp d y
 // so a row needs four sums (s^2, do pre_w s, y^2, cp d y) and a column two.
 //
-// Both directions move each value once and are bound by memory traffic.
+// Both directions move each value once: 8 and 12 bytes a bf16 value.  4096 x 6144
+// bf16 with both norms and a channel gate takes 37.5 us forward (5.4 TB/s, 82 % of a
+// copy's rate) and 66 us backward (4.6 TB/s; a row's chain of loads, sums and stores
+// in few warps is what is left); 64 tokens 3.1 and 9.8 us, which is launches.
 #include <algorithm>
 
 #include "coli_internal.cuh"
@@ -46,50 +49,110 @@ struct NormArgs {
     float* part;              // [grid][2][H] column partials: dpre_w, C
 };
 
-// VEC consecutive values starting at element i (16-byte aligned for VEC = 8).
-template <int VEC>
-__device__ __forceinline__ void load_vals(const void* p, int64_t i, int bf16, float* v) {
-    if constexpr (VEC == 8) {
-        if (bf16) {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// NCH vectors of VEC values as they lie in memory (whole vectors are aligned).
+// The loads stand apart from the conversions: a load whose type's branch also
+// converts it is waited for before the next one is issued (4096 x 1001 fp32
+// backward 56 us with the conversions inside, 41 us so).
+template <int VEC, int NCH>
+struct Raw {
+    uint32_t u[NCH][VEC];
+
+    // vectors at h(c), of a row's H values at element `row`; zeros past its end
+    // and where p is null
+    __device__ __forceinline__ void load(const void* p, int64_t row, int bf16, int H) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __uint_as_float(w[j] << 16);
-                v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) u[c][j] = 0;
+        if (!p) return;
+        if (bf16) {
+            const uint16_t* q = static_cast<const uint16_t*>(p) + row;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) {
+                const int h = column(c);
+                if (h >= H) continue;
+                if constexpr (VEC == 8) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(q + h);
+                    u[c][0] = x.x; u[c][1] = x.y; u[c][2] = x.z; u[c][3] = x.w;
+                } else if constexpr (VEC == 4) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(q + h);
+                    u[c][0] = x.x; u[c][1] = x.y;
+                } else {
+                    u[c][0] = q[h];
+                }
             }
         } else {
-            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            const uint32_t* q = static_cast<const uint32_t*>(p) + row;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) {
+                const int h = column(c);
+                if (h >= H) continue;
+                if constexpr (VEC == 1) {
+                    u[c][0] = q[h];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; j += 4) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(q + h + j);
+                        u[c][j] = x.x; u[c][j + 1] = x.y; u[c][j + 2] = x.z; u[c][j + 3] = x.w;
+                    }
+                }
+            }
         }
+    }
+    __device__ __forceinline__ void values(int bf16, float (&v)[NCH][VEC]) const {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const uint32_t w = u[c][j / 2];
+                v[c][j] = __uint_as_float(!bf16 ? u[c][j] : j & 1 ? w & 0xFFFF0000u : w << 16);
+            }
+    }
+    // first column of this thread's vector c
+    static __device__ __forceinline__ int column(int c) {
+        return (c * blockDim.x + threadIdx.x) * VEC;
+    }
+};
+
+// VEC of the fp32 weights, from column h on.
+template <int VEC>
+__device__ __forceinline__ void load_w(const float* p, int h, float* w) {
+    if constexpr (VEC == 1) {
+        w[0] = __ldg(p + h);
     } else {
-        v[0] = bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16)
-                    : static_cast<const float*>(p)[i];
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p + h + j));
+            w[j] = x.x; w[j + 1] = x.y; w[j + 2] = x.z; w[j + 3] = x.w;
+        }
     }
 }
 
 template <int VEC>
 __device__ __forceinline__ void store_vals(void* p, int64_t i, int bf16, const float* v) {
-    if constexpr (VEC == 8) {
-        if (bf16) {
-            uint4 u;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+    if (bf16) {
+        if constexpr (VEC == 1) {
+            static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v[0]);
+        } else {
+            uint32_t w[VEC / 2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < VEC / 2; ++j) {
                 const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
                 w[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = u;
-        } else {
-            float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+            uint16_t* q = static_cast<uint16_t*>(p) + i;
+            if constexpr (VEC == 8) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
         }
     } else {
-        if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v[0]);
-        else static_cast<float*>(p)[i] = v[0];
+        float* q = static_cast<float*>(p) + i;
+        if constexpr (VEC == 1) {
+            q[0] = v[0];
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; j += 4)
+                *reinterpret_cast<float4*>(q + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
     }
 }
 
@@ -117,6 +180,40 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* tmp) {
     }
 }
 
+// Block sums of N = 2 or 4 values over at most WARPS warps, in a fixed order.  The
+// first levels of the butterfly halve the values a lane carries instead of
+// reducing each of them: N - 1 + 5 - log2(N) shuffles a stage and not 5 N.
+template <int N, int WARPS>
+__device__ __forceinline__ void packed_sums(float (&v)[N], float* tmp) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    float x;
+    if constexpr (N == 4) {
+        const bool b0 = lane & 1, b1 = lane & 2;
+        const float k0 = (b0 ? v[1] : v[0]) + __shfl_xor_sync(kAll, b0 ? v[0] : v[1], 1);
+        const float k1 = (b0 ? v[3] : v[2]) + __shfl_xor_sync(kAll, b0 ? v[2] : v[3], 1);
+        x = (b1 ? k1 : k0) + __shfl_xor_sync(kAll, b1 ? k0 : k1, 2);
+    } else {
+        const bool b0 = lane & 1;
+        x = (b0 ? v[1] : v[0]) + __shfl_xor_sync(kAll, b0 ? v[0] : v[1], 1);
+    }
+#pragma unroll
+    for (int o = N; o < 32; o <<= 1) x += __shfl_xor_sync(kAll, x, o);
+    if (lane < N) tmp[lane * 32 + warp] = x;  // value `lane` of this warp
+    __syncthreads();
+    // 32 / N lanes to a value, each with its share of the warps
+    constexpr int kLanes = 32 / N;
+    const int k = lane / kLanes, i = lane % kLanes;
+    x = i < nw ? tmp[k * 32 + i] : 0.f;
+#pragma unroll
+    for (int j = kLanes; j < WARPS; j += kLanes)
+        if (i + j < nw) x += tmp[k * 32 + i + j];
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) x += __shfl_xor_sync(kAll, x, o);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = __shfl_sync(kAll, x, j * kLanes);
+}
+
 // One row per CTA, NCH chunks of VEC consecutive values per thread.
 template <int VEC, int NCH>
 __global__ void __launch_bounds__(VEC * NCH == 32 ? 512 : 1024)
@@ -128,15 +225,12 @@ block_norm_kernel(const NormArgs a) {
     const int64_t row = (int64_t)blockIdx.x * H;
     float v[NCH][VEC];
     float s[NCH][VEC];
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-        const int h = (c * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[c][j] = s[c][j] = 0.f;
-        if (h < H) {
-            if (a.y) load_vals<VEC>(a.y, row + h, a.y_bf16, v[c]);
-            load_vals<VEC>(a.x, row + h, a.x_bf16, s[c]);
-        }
+    {
+        Raw<VEC, NCH> ry, rx;
+        ry.load(a.y, row, a.y_bf16, H);
+        rx.load(a.x, row, a.x_bf16, H);
+        ry.values(a.y_bf16, v);
+        rx.values(a.x_bf16, s);
     }
     if (a.y) {
         float ry = 1.f;
@@ -156,12 +250,12 @@ block_norm_kernel(const NormArgs a) {
             if (h >= H) continue;
             float w[VEC];
             if (a.post_w) {
-                load_vals<VEC>(a.post_w, h, 0, w);
+                load_w<VEC>(a.post_w, h, w);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) v[c][j] *= ry * w[j];
             }
             if (a.gate_kind == COLI_GATE_CHANNEL) {
-                load_vals<VEC>(a.gate, h, 0, w);
+                load_w<VEC>(a.gate, h, w);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) v[c][j] *= w[j];
             }
@@ -189,7 +283,7 @@ block_norm_kernel(const NormArgs a) {
         const int h = (c * blockDim.x + threadIdx.x) * VEC;
         if (h >= H) continue;
         float w[VEC];
-        load_vals<VEC>(a.pre_w, h, 0, w);
+        load_w<VEC>(a.pre_w, h, w);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) w[j] *= s[c][j] * r;
         store_vals<VEC>(a.o, row + h, a.o_bf16, w);
@@ -200,9 +294,9 @@ block_norm_kernel(const NormArgs a) {
 // same columns for all of them, so the column sums stay in its registers and
 // leave as one partial row per CTA, summed by the next kernel in CTA order.
 template <int VEC, int NCH>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(VEC * NCH == 8 && VEC == 1 ? 768 : 512)
 block_norm_bwd_kernel(const NormArgs a) {
-    __shared__ float tmp[2][3 * 32];
+    __shared__ float tmp[2][4 * 32];
     pdl_wait();
     pdl_launch_dependents();
     const int H = a.H;
@@ -216,28 +310,25 @@ block_norm_bwd_kernel(const NormArgs a) {
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = (int64_t)t * H;
         float s[NCH][VEC], y[NCH][VEC], g[NCH][VEC], d[NCH][VEC];
-        float q[3] = {0.f, 0.f, 0.f};  // sum s^2, sum do pre_w s, sum y^2
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const int h = (c * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) s[c][j] = y[c][j] = g[c][j] = d[c][j] = 0.f;
-            if (h < H) {
-                if (a.go) {
-                    load_vals<VEC>(a.go, row + h, a.o_bf16, g[c]);
-                    load_vals<VEC>(a.s, row + h, a.x_bf16, s[c]);
-                }
-                if (a.gs) load_vals<VEC>(a.gs, row + h, a.x_bf16, d[c]);
-                if (a.y) load_vals<VEC>(a.y, row + h, a.y_bf16, y[c]);
-            }
+        {
+            Raw<VEC, NCH> rg, rs, rd, ry;
+            rg.load(a.go, row, a.o_bf16, H);
+            rs.load(a.go ? a.s : nullptr, row, a.x_bf16, H);
+            rd.load(a.gs, row, a.x_bf16, H);
+            ry.load(a.y, row, a.y_bf16, H);
+            rg.values(a.o_bf16, g);
+            rs.values(a.x_bf16, s);
+            rd.values(a.x_bf16, d);
+            ry.values(a.y_bf16, y);
         }
+        float q[4] = {0.f, 0.f, 0.f, 0.f};  // sum s^2, sum do pre_w s, sum y^2
         if (a.go) {
 #pragma unroll
             for (int c = 0; c < NCH; ++c) {
                 const int h = (c * blockDim.x + threadIdx.x) * VEC;
                 if (h >= H) continue;
                 float w[VEC];
-                load_vals<VEC>(a.pre_w, h, 0, w);
+                load_w<VEC>(a.pre_w, h, w);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     q[0] += s[c][j] * s[c][j];
@@ -251,7 +342,7 @@ block_norm_bwd_kernel(const NormArgs a) {
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) q[2] += y[c][j] * y[c][j];
         }
-        block_sums<3>(q, tmp[0]);
+        packed_sums<4, 32>(q, tmp[0]);
         const float r = rsqrtf(q[0] * inv_h + a.eps);
         const float ry = a.post_w ? rsqrtf(q[2] * inv_h + a.eps) : 1.f;
         const float rk = r * (r * r * (q[1] * inv_h));
@@ -264,7 +355,7 @@ block_norm_bwd_kernel(const NormArgs a) {
             if (h >= H) continue;
             float w[VEC];
             if (a.go) {
-                load_vals<VEC>(a.pre_w, h, 0, w);
+                load_w<VEC>(a.pre_w, h, w);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     c_pre[c][j] += (g[c][j] * s[c][j]) * r;
@@ -276,9 +367,9 @@ block_norm_bwd_kernel(const NormArgs a) {
                 float cp[VEC];
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) cp[j] = 1.f;
-                if (a.post_w) load_vals<VEC>(a.post_w, h, 0, cp);
+                if (a.post_w) load_w<VEC>(a.post_w, h, cp);
                 if (a.gate_kind == COLI_GATE_CHANNEL) {
-                    load_vals<VEC>(a.gate, h, 0, w);
+                    load_w<VEC>(a.gate, h, w);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) cp[j] *= w[j];
                 }
@@ -319,54 +410,23 @@ block_norm_bwd_kernel(const NormArgs a) {
 }
 
 // ---- many rows of whole 16-byte vectors ------------------------------------------
-// A CTA walks rows blockIdx.x, + gridDim.x, ... .  Each thread owns VPT vectors
+// A CTA walks rows blockIdx.x, + gridDim.x, ... .  Each thread owns kVpt vectors
 // of 8 columns and copies them (cp.async) into its own places of a ring in
 // shared memory, rows ahead of the one it works on, so that the memory system
 // has rows in flight whatever the row reductions wait for; nobody else reads
-// those places, so the copies need no barrier.  The weights of
-// a thread's columns lie in its registers (384 threads, H 6144) or in shared
-// memory (wider rows): read from L2 for every row they would be more bytes
-// than the row itself.  The types are template parameters and the loops have no branches
-// (a vector past the row's end has places of its own that nothing fills;
-// its sums are masked and its stores left out), so that a row's loads and sums interleave.
+// those places, so the copies need no barrier.  The weights of a thread's
+// columns lie in its registers (up to 384 threads, H 6144) or in shared memory
+// (wider rows): read from L2 for every row they would be more bytes than the row
+// itself.  The types are template parameters and the loops have no branches (a
+// vector past the row's end has places of its own that nothing fills; its sums
+// are masked and its stores left out), so that a row's loads and sums interleave.
 constexpr int kVpt = 2;                 // vectors per thread
 constexpr int kRingMaxThreads = 512;
 constexpr int kRegThreads = 384;        // up to these, the weights fit in registers
-
-// Block sums of N = 2 or 4 values over at most 16 warps, in a fixed order.  The
-// first levels of the butterfly halve the values a lane carries instead of
-// reducing each of them: N - 1 + 5 - log2(N) shuffles a stage and not 5 N.
-template <int N>
-__device__ __forceinline__ void ring_sums(float (&v)[N], float* tmp) {
-    constexpr unsigned kAll = 0xffffffffu;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    float x;
-    if constexpr (N == 4) {
-        const bool b0 = lane & 1, b1 = lane & 2;
-        const float k0 = (b0 ? v[1] : v[0]) + __shfl_xor_sync(kAll, b0 ? v[0] : v[1], 1);
-        const float k1 = (b0 ? v[3] : v[2]) + __shfl_xor_sync(kAll, b0 ? v[2] : v[3], 1);
-        x = (b1 ? k1 : k0) + __shfl_xor_sync(kAll, b1 ? k0 : k1, 2);
-    } else {
-        const bool b0 = lane & 1;
-        x = (b0 ? v[1] : v[0]) + __shfl_xor_sync(kAll, b0 ? v[0] : v[1], 1);
-    }
-#pragma unroll
-    for (int o = N; o < 32; o <<= 1) x += __shfl_xor_sync(kAll, x, o);
-    if (lane < N) tmp[lane * 32 + warp] = x;  // value `lane` of this warp
-    __syncthreads();
-    // 32 / N lanes to a value, each with its share of the warps
-    constexpr int kLanes = 32 / N;
-    const int k = lane / kLanes, i = lane % kLanes;
-    x = i < nw ? tmp[k * 32 + i] : 0.f;
-    if (kLanes < 16 && i + kLanes < nw) x += tmp[k * 32 + i + kLanes];
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) x += __shfl_xor_sync(kAll, x, o);
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = __shfl_sync(kAll, x, j * kLanes);
-}
+constexpr int kRegPairThreads = 256;    // and, backward, two CTAs in an SM
 
 // Pairs of fp32 values in one 64-bit register: one instruction for both.  (Issue
-// slots bound the scalar form: 52 and 91 us at 4096 x 6144 bf16.)
+// slots bound the same kernels on single values: 52 and 91 us at 4096 x 6144 bf16.)
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pair(float lo, float hi) {
     f2 r;
@@ -538,14 +598,14 @@ struct Weights {
                 float w[8], g[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = 1.f;
-                if (a.pre_w) load_vals<8>(a.pre_w, h, 0, w);
+                if (a.pre_w) load_w<8>(a.pre_w, h, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[0][c][j] = pair(w[2 * j], w[2 * j + 1]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) w[j] = 1.f;
-                if (a.post_w) load_vals<8>(a.post_w, h, 0, w);
+                if (a.post_w) load_w<8>(a.post_w, h, w);
                 if (a.gate_kind == COLI_GATE_CHANNEL) {
-                    load_vals<8>(a.gate, h, 0, g);
+                    load_w<8>(a.gate, h, g);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) w[j] *= g[j];
                 }
@@ -599,12 +659,11 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, const __grid_constant
     if (a.post_w) {
         cp_async_wait_n(p.slots - 1);
         q[1] = sum_y(0);
-        ring_sums<2>(q, tmp[1]);
+        packed_sums<2, 16>(q, tmp[1]);
     }
     int slot = 0, odd = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        // this row and the next one are in the ring
-        cp_async_wait_n(p.slots - 2);
+        cp_async_wait_n(p.slots - 2);  // this row and the next one are in the ring
         const int64_t row = t * H;
         const int after = slot + 1 == p.slots ? 0 : slot + 1;
         f2 s[kVpt][4];
@@ -636,7 +695,7 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, const __grid_constant
         q[1] = a.post_w ? sum_y(after) : 0.f;
         // the slot is read: fetch the row that takes its place
         ring.fetch<XB, YB, false, false>(t + (int64_t)p.slots * gridDim.x, slot);
-        if (a.o || a.post_w) ring_sums<2>(q, tmp[odd]);
+        if (a.o || a.post_w) packed_sums<2, 16>(q, tmp[odd]);
         if (a.o) {
             const float r = rsqrtf(q[0] * inv_h + a.eps);
             const f2 r2 = pair(r, r);
@@ -654,12 +713,16 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, const __grid_constant
     }
 }
 
-template <bool REG, bool XB, bool YB, bool OB>
-__global__ void __launch_bounds__(REG ? kRegThreads : kRingMaxThreads)
+// THREADS: the most it is launched with.  Two CTAs of 256 threads fit an SM with 128
+// registers each (4096 x 4096 bf16: 47 us, one CTA of 138 registers 58), one of 384
+// is better off with all it can use (4096 x 6144: 66 us, with 128 registers 73).
+template <int THREADS, bool XB, bool YB, bool OB>
+__global__ void __launch_bounds__(THREADS, THREADS <= kRegPairThreads ? 2 : 1)
 block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
                            const __grid_constant__ RingPlan p) {
     extern __shared__ __align__(128) char smem[];
     __shared__ float tmp[2][4 * 32];
+    constexpr bool REG = THREADS <= kRegThreads;
     const int H = a.H;
     const RowRing ring{p, smem + p.weights, H, a.T};
     const float inv_h = 1.f / (float)H;
@@ -711,11 +774,9 @@ block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
     cp_async_wait_n(p.slots - 1);
     first_sums(0, q);
     q[3] = 0.f;
-    ring_sums<4>(q, tmp[1]);
+    packed_sums<4, 16>(q, tmp[1]);
     int slot = 0, odd = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        // this row and the next one are in the ring
-        cp_async_wait_n(p.slots - 2);
         const int64_t row = t * H;
         const int after = slot + 1 == p.slots ? 0 : slot + 1;
         float gt = 1.f;
@@ -757,8 +818,9 @@ block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
                 q[3] += ring.live(c) ? sum2(z) : 0.f;
             }
         }
+        cp_async_wait_n(p.slots - 2);  // the next row is in the ring
         first_sums(after, q);
-        ring_sums<4>(q, tmp[odd]);
+        packed_sums<4, 16>(q, tmp[odd]);
         if (a.y) {
             const float c1 = ry * A;
             const float c2 = a.post_w ? -ry * (ry * ry * (A * q[3] * inv_h)) : 0.f;
@@ -790,13 +852,16 @@ block_norm_bwd_ring_kernel(const __grid_constant__ NormArgs a,
     }
 }
 
-// Column sums over the CTAs' partial rows, 32 columns per block, 8 warps over
+// Column sums over the CTAs' partial rows, 32 columns per block, 16 warps over
 // the CTAs; fixed order (each warp its strided share ascending, then the warps
-// ascending).  blockIdx.y 0: dpre_w, 1: C, from which dpost_w and a channel
-// gate's dgate follow.
-__global__ void __launch_bounds__(256)
+// ascending).  A warp has kColBatch loads in flight (of the last row again where
+// there are no more): one round of L2 latency for 160 partial rows.  blockIdx.y
+// 0: dpre_w, 1: C, from which dpost_w and a channel gate's dgate follow.
+constexpr int kColBatch = 10, kColWarps = 16;
+
+__global__ void __launch_bounds__(kColWarps * 32)
 norm_columns_kernel(const NormArgs a, int n_part) {
-    __shared__ float acc[8][32];
+    __shared__ float acc[kColWarps][32];
     pdl_wait();
     pdl_launch_dependents();
     const bool channel = a.gate_kind == COLI_GATE_CHANNEL;
@@ -807,14 +872,20 @@ norm_columns_kernel(const NormArgs a, int n_part) {
     float v = 0.f;
     if (h < a.H) {
         const float* p = a.part + (int64_t)blockIdx.y * a.H + h;
-#pragma unroll 4
-        for (int i = warp; i < n_part; i += 8) v += p[(int64_t)i * 2 * a.H];
+        for (int i0 = warp; i0 < n_part; i0 += kColWarps * kColBatch) {
+            float f[kColBatch];
+#pragma unroll
+            for (int j = 0; j < kColBatch; ++j)
+                f[j] = p[(int64_t)min(i0 + kColWarps * j, n_part - 1) * 2 * a.H];
+#pragma unroll
+            for (int j = 0; j < kColBatch; ++j) v += i0 + kColWarps * j < n_part ? f[j] : 0.f;
+        }
     }
     acc[warp][lane] = v;
     __syncthreads();
     if (warp != 0 || h >= a.H) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) v += acc[w][lane];
+    for (int w = 1; w < kColWarps; ++w) v += acc[w][lane];
     if (blockIdx.y == 0) {
         a.dpre_w[h] = v;
     } else {
@@ -842,18 +913,24 @@ coli_status check_norm(int32_t T, int32_t H, int32_t gate_kind, const void* gate
 
 // CTAs of the backward kernels, at most (each leaves one partial row of column
 // sums in the workspace).
-constexpr int kMaxBwdCtas = 3 * 148;
-int norm_bwd_ctas(int T) { return std::max(1, std::min(T, kMaxBwdCtas)); }
+int norm_bwd_ctas(int T, int H) { return std::max(1, std::min(T, (H <= 512 ? 6 : 3) * 148)); }
 
-// Widths and rows per CTA from which the ring kernels pay: below them the
-// weights' way into shared memory costs more than the rows gain.
-constexpr int kRingMinH = 512, kRingRows = 3;
+// Where the ring kernels pay: enough values that the rows gain more than the
+// ring's start costs.  bf16, ring against one row a CTA, forward: 450 rows of 2048
+// 3.9 and 3.2 us, 900 of them 4.9 and 5.2; 300 of 4096 4.4 and 5.2, 200 of them 4.0
+// and 3.3; 4096 rows of 768 10.4 and 7.0.  Backward: 300 rows of 768 7.7 and 6.6,
+// 600 of them 8.7 and 9.1; 200 of 2048 7.7 and 10.3; 4096 of 6144 66 and 113.
+constexpr int kRingMinH = 512, kRingFwdMinH = 1536;
+constexpr int64_t kRingFwdValues = 1 << 20, kRingBwdValues = 400000;
 
 // The ring kernels' launch for these arrays: threads, CTAs per SM and ring depth,
-// or false where the row is too wide, not of whole vectors, or the rows too few.
-bool plan_ring(const NormArgs& a, const void* const (&src)[4], const int (&bf16)[4], RingPlan* p,
-               int* threads, int* grid, int* smem) {
-    if (a.H % 8 || a.H < kRingMinH || a.H > 8 * kVpt * kRingMaxThreads) return false;
+// or false where the row is too wide, not of whole vectors, or the values too few.
+bool plan_ring(bool backward, const NormArgs& a, const void* const (&src)[4],
+               const int (&bf16)[4], RingPlan* p, int* threads, int* grid, int* smem) {
+    if (a.H % 8 || a.H < (backward ? kRingMinH : kRingFwdMinH) ||
+        a.H > 8 * kVpt * kRingMaxThreads ||
+        (int64_t)a.T * a.H < (backward ? kRingBwdValues : kRingFwdValues))
+        return false;
     *threads = ((a.H + 8 * kVpt - 1) / (8 * kVpt) + 31) / 32 * 32;
     *p = RingPlan{};
     uint32_t slot = 0;
@@ -866,44 +943,61 @@ bool plan_ring(const NormArgs& a, const void* const (&src)[4], const int (&bf16)
     p->slot = (slot + 127) / 128 * 128;
     p->weights =
         *threads <= kRegThreads ? 0 : (uint32_t)(2 * sizeof(float) * a.H + 127) / 128 * 128;
-    for (int per_sm = std::max(1, std::min(3, 768 / *threads)); per_sm >= 1; --per_sm) {
+    // threads that the register file holds: 74 registers each, 128 backward
+    const int resident = backward ? 512 : 768;
+    for (int per_sm = std::max(1, std::min(3, resident / *threads)); per_sm >= 1; --per_sm) {
         const int budget = 224 * 1024 / per_sm - 2048;
         const int slots = std::min(7, (budget - (int)p->weights) / (int)p->slot);
-        if (slots < 3) continue;  // two rows in hand, one on its way
+        // two rows in hand, one on its way; one CTA of very wide rows does with two
+        if (slots < (per_sm == 1 ? 2 : 3)) continue;
         p->slots = slots;
         *grid = 148 * per_sm;
         *smem = (int)(p->weights + slots * p->slot);
-        if (a.T < *grid * kRingRows) continue;
-        return true;
+        // (backward, each CTA has partial sums to leave: 450 rows of 2048 take 10.3
+        // us with 148 CTAs, 10.7 with 444; 900 of them 13.9 with 296, 12.9 with 444)
+        if (a.T >= *grid * (backward && per_sm > 1 ? 2 : 1)) return true;
     }
     return false;
 }
 
-template <bool REG, bool XB, bool YB, bool OB>
+template <int THREADS, bool XB, bool YB, bool OB>
 cudaError_t launch_ring(bool backward, const NormArgs& a, const RingPlan& p, int threads, int grid,
                         int smem, cudaStream_t st) {
-    auto kernel = backward ? block_norm_bwd_ring_kernel<REG, XB, YB, OB>
-                           : block_norm_ring_kernel<REG, XB, YB, OB>;
+    auto kernel = backward ? block_norm_bwd_ring_kernel<THREADS, XB, YB, OB>
+                           : block_norm_ring_kernel<THREADS <= kRegThreads, XB, YB, OB>;
     const cudaError_t err =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     return launch_serialized(kernel, dim3(grid), dim3(threads), smem, st, a, p);
 }
 
-template <bool REG>
-cudaError_t dispatch_ring(bool backward, const NormArgs& a, const RingPlan& p, int threads, int grid,
-                          int smem, cudaStream_t st) {
+template <int THREADS>
+cudaError_t dispatch_types(bool backward, const NormArgs& a, const RingPlan& p, int threads,
+                           int grid, int smem, cudaStream_t st) {
     using Fn = cudaError_t (*)(bool, const NormArgs&, const RingPlan&, int, int, int, cudaStream_t);
     static const Fn fn[2][2][2] = {
-        {{launch_ring<REG, false, false, false>, launch_ring<REG, false, false, true>},
-         {launch_ring<REG, false, true, false>, launch_ring<REG, false, true, true>}},
-        {{launch_ring<REG, true, false, false>, launch_ring<REG, true, false, true>},
-         {launch_ring<REG, true, true, false>, launch_ring<REG, true, true, true>}}};
+        {{launch_ring<THREADS, false, false, false>, launch_ring<THREADS, false, false, true>},
+         {launch_ring<THREADS, false, true, false>, launch_ring<THREADS, false, true, true>}},
+        {{launch_ring<THREADS, true, false, false>, launch_ring<THREADS, true, false, true>},
+         {launch_ring<THREADS, true, true, false>, launch_ring<THREADS, true, true, true>}}};
     return fn[a.x_bf16 != 0][a.y_bf16 != 0][a.o_bf16 != 0](backward, a, p, threads, grid, smem, st);
 }
 
-// Chunks per thread: rows of whole 8-value vectors use 16-byte accesses, other
-// widths one value at a time.
+cudaError_t dispatch_ring(bool backward, const NormArgs& a, const RingPlan& p, int threads, int grid,
+                          int smem, cudaStream_t st) {
+    if (threads <= kRegPairThreads)
+        return dispatch_types<kRegPairThreads>(backward, a, p, threads, grid, smem, st);
+    if (threads <= kRegThreads)
+        return dispatch_types<kRegThreads>(backward, a, p, threads, grid, smem, st);
+    return dispatch_types<kRingMaxThreads>(backward, a, p, threads, grid, smem, st);
+}
+
+// Vectors and threads: 16-byte accesses where all rows start on 16 bytes whatever
+// their type, 16 or 8 bytes where H is a multiple of 4, else one value at a time.
+// Wider rows take more values a thread, up to what the registers hold (fp32, 4096
+// rows, forward and backward: 2001 values by 8 a thread 24.8 and 59.5 us, by 4 28.5
+// and 83.9; 1001 by 8 13.9 and 49.8, by 4 14.8 and 41.1; 2004 in 4 vectors a thread
+// 21.1 and 43.9, in 2 19.9 and 60.4).
 template <template <int, int> class Launch>
 cudaError_t dispatch_width(int H, int max_threads, const NormArgs& a, int grid, cudaStream_t st) {
     auto threads = [&](int vec, int nch) { return ((H + vec * nch - 1) / (vec * nch) + 31) / 32 * 32; };
@@ -912,7 +1006,13 @@ cudaError_t dispatch_width(int H, int max_threads, const NormArgs& a, int grid, 
         if (threads(8, 2) <= max_threads) return Launch<8, 2>::run(a, grid, threads(8, 2), st);
         return Launch<8, 4>::run(a, grid, threads(8, 4), st);
     }
-    if (threads(1, 4) <= 512) return Launch<1, 4>::run(a, grid, threads(1, 4), st);
+    if (H % 4 == 0) {
+        if (H <= 1024) return Launch<4, 2>::run(a, grid, threads(4, 2), st);
+        if (threads(4, 4) <= 512) return Launch<4, 4>::run(a, grid, threads(4, 4), st);
+        return Launch<4, 8>::run(a, grid, threads(4, 8), st);
+    }
+    if (H <= 1024) return Launch<1, 4>::run(a, grid, threads(1, 4), st);
+    if (threads(1, 8) <= 768) return Launch<1, 8>::run(a, grid, threads(1, 8), st);
     return Launch<1, 32>::run(a, grid, threads(1, 32), st);
 }
 
@@ -965,9 +1065,8 @@ coli_status coli_moe_block_norm(int32_t T, int32_t H, const void* x, coli_out_dt
     RingPlan p;
     int threads, grid, smem;
     cudaError_t err;
-    if (plan_ring(a, src, bf16, &p, &threads, &grid, &smem))
-        err = (threads <= kRegThreads ? dispatch_ring<true> : dispatch_ring<false>)(
-            false, a, p, threads, grid, smem, st);
+    if (plan_ring(false, a, src, bf16, &p, &threads, &grid, &smem))
+        err = dispatch_ring(false, a, p, threads, grid, smem, st);
     else
         err = dispatch_width<Forward>(H, T <= 148 ? 1024 : 512, a, T, st);
     return err == cudaSuccess ? COLI_OK : COLI_ERR_CUDA;
@@ -975,7 +1074,7 @@ coli_status coli_moe_block_norm(int32_t T, int32_t H, const void* x, coli_out_dt
 
 size_t coli_moe_block_norm_workspace_size(int32_t T, int32_t H) {
     if (T < 0 || H <= 0) return 0;
-    return kHeaderBytes + sizeof(float) * 2 * (size_t)H * (size_t)norm_bwd_ctas(T);
+    return kHeaderBytes + sizeof(float) * 2 * (size_t)H * (size_t)norm_bwd_ctas(T, H);
 }
 
 coli_status coli_moe_block_norm_backward(
@@ -1024,16 +1123,15 @@ coli_status coli_moe_block_norm_backward(
     RingPlan p;
     int threads, smem, grid;
     cudaError_t err;
-    if (plan_ring(a, src, bf16, &p, &threads, &grid, &smem)) {
-        err = (threads <= kRegThreads ? dispatch_ring<true> : dispatch_ring<false>)(
-            true, a, p, threads, grid, smem, st);
+    if (plan_ring(true, a, src, bf16, &p, &threads, &grid, &smem)) {
+        err = dispatch_ring(true, a, p, threads, grid, smem, st);
     } else {
-        grid = norm_bwd_ctas(T);
+        grid = norm_bwd_ctas(T, H);
         err = dispatch_width<Backward>(H, 512, a, grid, st);
     }
     if (err == cudaSuccess && columns)
-        err = launch_serialized(norm_columns_kernel, dim3((H + 31) / 32, 2), dim3(256), 0, st, a,
-                                grid);
+        err = launch_serialized(norm_columns_kernel, dim3((H + 31) / 32, 2), dim3(kColWarps * 32), 0,
+                                st, a, grid);
     return err == cudaSuccess ? COLI_OK : COLI_ERR_CUDA;
 }
 

@@ -77,6 +77,15 @@ CASES = [  # T, H, x type, y type, norm after the block, gate
     (700, 8192, torch.bfloat16, torch.bfloat16, True, "token"),
     (1500, 40, torch.bfloat16, torch.float32, True, "channel"),
     (3001, 2048, torch.bfloat16, torch.bfloat16, False, "none"),
+    (300, 6144, torch.float32, torch.float32, True, "token"),    # two rows in the ring
+    (310, 4096, torch.bfloat16, torch.float32, True, "channel"),
+    # rows of 4-value vectors and of single values, over the widths of each form
+    (40, 604, torch.float32, torch.bfloat16, True, "channel"),
+    (333, 2004, torch.bfloat16, torch.float32, False, "token"),
+    (160, 6140, torch.bfloat16, torch.bfloat16, True, "channel"),
+    (2, 16380, torch.float32, torch.float32, True, "none"),
+    (900, 505, torch.bfloat16, torch.bfloat16, True, "token"),
+    (470, 3001, torch.float32, torch.float32, True, "none"),
 ]
 
 
