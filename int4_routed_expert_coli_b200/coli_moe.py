@@ -308,7 +308,7 @@ def _device(*tensors):
 
 def _run(fn, device, stream, *args):
     """fn(*args, stream) on `device`, by default on its current stream."""
-    current = torch.cuda.current_device()
+    current = torch._C._cuda_getDevice()  # (a tensor is on a device: CUDA is set up)
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(device)
     else:
@@ -323,6 +323,8 @@ def _ws_arg(ws, device):
     """(pointer, bytes) of a workspace tensor of any type; (None, 0) for None."""
     if ws is None:
         return None, 0
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws: expected a torch.Tensor")
     n = ws.numel()
     return _arg(ws, "ws", n, (ws.dtype,), device), ws.nbytes
 

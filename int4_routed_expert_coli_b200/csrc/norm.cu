@@ -422,6 +422,7 @@ block_norm_bwd_kernel(const NormArgs a) {
 // are masked and its stores left out), so that a row's loads and sums interleave.
 constexpr int kVpt = 2;                 // vectors per thread
 constexpr int kRingMaxThreads = 512;
+constexpr int kRingSmem = 222 * 1024;   // dynamic shared memory of a CTA, at most
 constexpr int kRegThreads = 384;        // up to these, the weights fit in registers
 constexpr int kRegPairThreads = 256;    // and, backward, two CTAs in an SM
 
@@ -946,7 +947,7 @@ bool plan_ring(bool backward, const NormArgs& a, const void* const (&src)[4],
     // threads that the register file holds: 74 registers each, 128 backward
     const int resident = backward ? 512 : 768;
     for (int per_sm = std::max(1, std::min(3, resident / *threads)); per_sm >= 1; --per_sm) {
-        const int budget = 224 * 1024 / per_sm - 2048;
+        const int budget = (kRingSmem + 2048) / per_sm - 2048;
         const int slots = std::min(7, (budget - (int)p->weights) / (int)p->slot);
         // two rows in hand, one on its way; one CTA of very wide rows does with two
         if (slots < (per_sm == 1 ? 2 : 3)) continue;
@@ -965,8 +966,9 @@ cudaError_t launch_ring(bool backward, const NormArgs& a, const RingPlan& p, int
                         int smem, cudaStream_t st) {
     auto kernel = backward ? block_norm_bwd_ring_kernel<THREADS, XB, YB, OB>
                            : block_norm_ring_kernel<THREADS <= kRegThreads, XB, YB, OB>;
-    const cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done[2];
+    const cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), kRingSmem,
+                                       done[backward]);
     if (err != cudaSuccess) return err;
     return launch_serialized(kernel, dim3(grid), dim3(threads), smem, st, a, p);
 }
