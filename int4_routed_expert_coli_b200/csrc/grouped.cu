@@ -62,10 +62,10 @@ constexpr int kChunk = 12;             // bf16 K-blocks per accumulator chain, a
 constexpr int kScaleBufs = 4;          // handovers whose column scales are loaded ahead
 constexpr int kScaleRing = 8;          // kFwdRows: K-blocks whose scales are loaded ahead
 constexpr int kSmemMax = 227 * 1024;
-// The last wave is cut into ranges of kMinRange K-blocks at least, and not at
-// all where a whole tile costs a worker at most kCutCost K-blocks more than its
-// range: partial sums take about 5 us to leave and be added up, a K-block 0.4.
-constexpr int kMinRange = 12, kCutCost = 12;
+// The last wave is cut into ranges of kMinRange K-blocks at least, and not at all
+// where a whole tile costs a worker at most Cfg::kCutCost K-blocks more than its
+// range.
+constexpr int kMinRange = 12;
 constexpr int kBand = 8;
 // kDw: a warp's stores leave through kStoreBufs stagings of 32 rows x 64 bytes
 constexpr int kStoreBytes = 32 * 64, kStoreBufs = 3;
@@ -115,6 +115,12 @@ struct Cfg {
     // whose weights come in 0.2.
     static constexpr int kBatch = kColScale ? 4 : 1;
     static constexpr int kBufs = kTmemAll / (BN * kBatch);      // handovers under way
+    // What partial sums cost, in K-blocks: a narrow tile's are 32 KB a CTA, a wide
+    // one's 128 KB, about 15 us to leave and be added up.  With 12 for all, whole
+    // tiles being better: 2048 rows of 8 groups, N 512, K 2048 bf16 30.4 us and 20.2,
+    // 600 rows of 3 groups of 4096 x 6144 54 and 44, 300 x 2048 x 2048 (narrow) 17.5
+    // and 14.1, 512 x 4096 x 4096 e4m3 31 and 26.
+    static constexpr int kCutCost = BN <= 64 ? 32 : FP8 ? 24 : 40;
     static constexpr int kNGrain = 16 * CTAS;              // MMA N in multiples of this
     static constexpr bool kAMn = MODE == kDx || MODE == kDw;
     static constexpr bool kBMn = MODE == kDw;
@@ -224,7 +230,7 @@ struct Walk {
         }
         const int wave = (int)(steps - base);
         const int range = max(kMinRange, (wave + workers() - 1) / workers());
-        const bool cut = s.kb_max > range + kCutCost;
+        const bool cut = s.kb_max > range + C::kCutCost;
         s.whole = (int)(cut ? full : tiles);
         s.base = base;
         s.wave = cut ? wave : 0;
@@ -1126,7 +1132,14 @@ coli_status launch_mm(const void* A, const void* B, MmArgs a, int N, int K, cuda
 // 34.8 us, of 128 rows 38.9 (narrow 32.8); 32 groups of 32 rows on average 266 and
 // 279 us, of 48 rows 276 and 283, of 64 rows 297 and 285 (e4m3: 156 and 167, 174
 // and 170, 195 and 176).
-bool narrow(int R, int E) { return (int64_t)R <= 48 * (int64_t)E + 16; }
+// And where they make a wave at most: wide ones would leave SMs without work (1024
+// x 1024 x 1024 narrow 9.7 us, wide 14.7; 2217 rows of 5 groups, N 472, K 1624 14.0
+// and 20.3, with more than a wave, for their 1624 columns, 18.1 and 14.5; 2048 x
+// 1024 x 2048, 1.7 waves, 23.7 and 20.1).
+bool narrow(int R, int E, int M) {
+    const int64_t rows = (int64_t)R + 32 * (int64_t)E;  // half a tile lost per group
+    return (int64_t)R <= 48 * (int64_t)E + 16 || rows * ((M + kBM - 1) / kBM) <= 64 * 160;
+}
 
 constexpr size_t kPartBytes = sizeof(float) * kMaxGrid * 2 * kBM * 256;
 
@@ -1185,7 +1198,7 @@ coli_status coli_moe_grouped_mm(int32_t R, int32_t E, int32_t N, int32_t K, cons
     if (s != COLI_OK) return s;
     const MmArgs a = make_mm_args(offsets, R, E, N, K, out, out_dtype, ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return narrow(R, E) ? launch_mm<kFwd, false, 64, 1>(w_bf16, x_bf16, a, N, K, st)
+    return narrow(R, E, N) ? launch_mm<kFwd, false, 64, 1>(w_bf16, x_bf16, a, N, K, st)
                         : launch_mm<kFwd, false, 256, 2>(w_bf16, x_bf16, a, N, K, st);
 }
 
@@ -1199,7 +1212,7 @@ coli_status coli_moe_grouped_mm_dx(int32_t R, int32_t E, int32_t N, int32_t K, c
     if (s != COLI_OK) return s;
     const MmArgs a = make_mm_args(offsets, R, E, K, N, dx, dx_dtype, ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return narrow(R, E) ? launch_mm<kDx, false, 64, 1>(w_bf16, dy_bf16, a, N, K, st)
+    return narrow(R, E, K) ? launch_mm<kDx, false, 64, 1>(w_bf16, dy_bf16, a, N, K, st)
                         : launch_mm<kDx, false, 256, 2>(w_bf16, dy_bf16, a, N, K, st);
 }
 
@@ -1238,7 +1251,7 @@ coli_status coli_moe_fp8_grouped_mm(int32_t R, int32_t E, int32_t N, int32_t K, 
     a.xs = x_scale;
     a.ws = w_scale;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return narrow(R, E) ? launch_mm<kFwd, true, 64, 1>(wq, xq, a, N, K, st)
+    return narrow(R, E, N) ? launch_mm<kFwd, true, 64, 1>(wq, xq, a, N, K, st)
                         : launch_mm<kFwdRows, true, 256, 1>(xq, wq, a, N, K, st);
 }
 
