@@ -51,6 +51,11 @@ SHAPES = [
     ([40] * 20, 128, 128),
     ([513], 256, 6144),
     ([2048, 5], 520, 136),
+    # more than a wave of narrow tiles: wide ones, in pairs of CTAs
+    ([65, 700, 0, 33, 2], 1608, 1544),
+    ([3000], 520, 200),
+    ([2048, 5, 9], 776, 1000),
+    ([513], 2312, 6144),
 ]
 
 
