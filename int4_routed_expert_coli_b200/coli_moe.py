@@ -296,6 +296,12 @@ _F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
+def _int32(*sizes):
+    """Sizes are passed in 32 bits: larger ones would arrive as other numbers."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes {sizes} do not fit 32 bits")
+
+
 def _device(*tensors):
     """Index of the CUDA device of the first tensor given."""
     for t in tensors:
@@ -333,6 +339,7 @@ def coli_moe_block_norm(T, H, x, y, post_w, gate, gate_kind, alpha, pre_w, eps, 
                         stream=None, raise_on_error=True):
     """s = x + alpha * g * norm(y) post_w;  o = norm(s) pre_w (include/coli_moe.h).
     x and s_out share one type, y and o have their own (fp32 or bf16)."""
+    _int32(T, H)
     dev = _device(x, s_out, o)
     n = T * H
     args = (T, H, _arg(x, "x", n, _DTYPE, dev), _DTYPE[x.dtype],
@@ -347,6 +354,7 @@ def coli_moe_block_norm(T, H, x, y, post_w, gate, gate_kind, alpha, pre_w, eps, 
 
 
 def coli_moe_block_norm_workspace_size(T, H):
+    _int32(T, H)
     return int(lib.coli_moe_block_norm_workspace_size(T, H))
 
 
@@ -355,6 +363,7 @@ def coli_moe_block_norm_backward(T, H, d_o, d_s, s, y, post_w, gate, gate_kind, 
                                  raise_on_error=True):
     """Gradients of coli_moe_block_norm from the stored s and y
     (include/coli_moe.h)."""
+    _int32(T, H)
     dev = _device(d_o, d_s, s, y, dx, dy, dpre_w, dpost_w, dgate)
     n = T * H
     stream_t = next((t for t in (s, d_s, dx) if t is not None), None)
@@ -379,6 +388,7 @@ def coli_moe_block_norm_backward(T, H, d_o, d_s, s, y, post_w, gate, gate_kind, 
 
 
 def coli_moe_grouped_workspace_size(R, E):
+    _int32(R, E)
     return int(lib.coli_moe_grouped_workspace_size(R, E))
 
 
@@ -392,6 +402,7 @@ def grouped_workspace(R, E, device="cuda"):
 
 def coli_moe_grouped_mm(R, E, N, K, x, w, offsets, out, ws, stream=None, raise_on_error=True):
     """out[r] = w[e] x[r] for the rows of each expert (include/coli_moe.h)."""
+    _int32(R, E, N, K)
     dev = _device(x, w, out)
     s = _run(lib.coli_moe_grouped_mm, dev, stream, R, E, N, K, _arg(x, "x", R * K, _BF16, dev),
              _arg(w, "w", E * N * K, _BF16, dev), _arg(offsets, "offsets", E + 1, _I32, dev),
@@ -401,6 +412,7 @@ def coli_moe_grouped_mm(R, E, N, K, x, w, offsets, out, ws, stream=None, raise_o
 
 def coli_moe_grouped_mm_dx(R, E, N, K, dy, w, offsets, dx, ws, stream=None, raise_on_error=True):
     """dx[r] = w[e]^T dy[r] (include/coli_moe.h)."""
+    _int32(R, E, N, K)
     dev = _device(dy, w, dx)
     s = _run(lib.coli_moe_grouped_mm_dx, dev, stream, R, E, N, K,
              _arg(dy, "dy", R * N, _BF16, dev), _arg(w, "w", E * N * K, _BF16, dev),
@@ -412,6 +424,7 @@ def coli_moe_grouped_mm_dx(R, E, N, K, dy, w, offsets, dx, ws, stream=None, rais
 def coli_moe_grouped_mm_dw(R, E, N, K, dy, x, offsets, dw, accumulate, ws, stream=None,
                            raise_on_error=True):
     """dw[e] (+)= sum over the rows of e of dy[r] x[r]^T (include/coli_moe.h)."""
+    _int32(R, E, N, K)
     dev = _device(dy, x, dw)
     s = _run(lib.coli_moe_grouped_mm_dw, dev, stream, R, E, N, K,
              _arg(dy, "dy", R * N, _BF16, dev), _arg(x, "x", R * K, _BF16, dev),
@@ -423,6 +436,7 @@ def coli_moe_grouped_mm_dw(R, E, N, K, dy, x, offsets, dw, accumulate, ws, strea
 def coli_moe_fp8_quantize_rows(R, K, x, q, scales, stream=None, raise_on_error=True):
     """Rows to e4m3 with one fp32 scale per row and 128 values; scales is
     [ceil(K/128)][R] (include/coli_moe.h)."""
+    _int32(R, K)
     dev = _device(x, q, scales)
     s = _run(lib.coli_moe_fp8_quantize_rows, dev, stream, R, K, _arg(x, "x", R * K, _DTYPE, dev),
              _DTYPE[x.dtype], _arg(q, "q", R * K, _E4M3, dev),
@@ -434,6 +448,7 @@ def coli_moe_fp8_grouped_mm(R, E, N, K, xq, x_scale, wq, w_scale, offsets, out, 
                             raise_on_error=True):
     """The grouped product of e4m3 rows and weights with their block scales
     (include/coli_moe.h)."""
+    _int32(R, E, N, K)
     dev = _device(xq, wq, out)
     kb = -(-K // 128)
     s = _run(lib.coli_moe_fp8_grouped_mm, dev, stream, R, E, N, K,

@@ -8,25 +8,43 @@
 //
 // The long, regular dimension (weight rows; the weights' columns for kDx) is
 // the MMA M (128 per CTA), the ragged rows are N (up to BN, in multiples of
-// 16, so a group of 130 rows costs 144 and not two tiles of 128); kDw has
+// 16 per CTA, so a group of 130 rows costs 160 and not two tiles of 128); kDw has
 // n as M, k as N and the rows as the reduction.  Operands are read as they lie
 // in memory: an operand whose reduction index is the slow one (w of kDx, both
-// of kDw) is an MN-major tile, so no transposed copy exists.
+// of kDw) is an MN-major tile, so no transposed copy exists.  Wide e4m3 products
+// have the rows as M (kFwdRows): a thread then drains one row, with one scale a
+// K-block, and not one for each of its columns (4096 rows of 32 experts of 4096 x
+// 6144: 199 us, with the weights as M 291).
 //
-// One CTA per SM, persistent; warp 0 loads (tensor copies, a ring of stages
-// of 128 bytes x rows), warp 1 issues the MMAs, the last eight warps drain the
-// accumulators.  Tensor memory holds two accumulators; the MMAs of one run
-// while the other is drained:
+// One CTA per SM, persistent; one thread of warp 0 loads (tensor copies into a
+// ring of stages of 128 bytes x rows), one of warp 1 issues the MMAs, warp 2 copies
+// scales or clears rows, eight warps drain the accumulators, of which tensor
+// memory holds two or more; the MMAs of one run while another is drained:
 //   * a bf16 sum is drained into fp32 registers every kChunk K-blocks at most:
 //     the tensor cores' fp32 accumulation truncates, and a chain of 6144
 //     products is 7e-6 off (16384: 2e-5), one of 768 below 1e-6;
 //   * an e4m3 sum is drained every block of 128, times the block's two scales
-//     (the row's and the weight block's; a tile's 128 weight rows are one scale
-//     block), which are copied ahead into shared memory.
+//     (the row's and the weight block's; 128 weight rows are one scale block),
+//     which are copied ahead into shared memory.
+// bf16 tiles are 256 x 256 by a pair of CTAs (each loads its half of both operands:
+// a K-block of 64 is 32 KB a CTA for 128 x 256 x 64), or 128 x 64 by one where the
+// weights' stream bounds the call or few tiles would leave SMs idle (`narrow`).
 //
-// Tiles: whole waves of tiles are dealt to the CTAs in order; the tiles of the
-// last, incomplete wave are dealt as one sequence of K-blocks, cut into equal
-// ranges, so few tiles (one token's experts) still use every SM.  A tile cut
+// What bounds them, and the measured times (B200, one call between L2 flushes):
+//   * 8192 x 6144 x 6144 bf16 400 us, 1.54 PFLOP/s: the tensor cores at the clock
+//     the power limit leaves; e4m3 373 us: the drain, whose round trip (commit,
+//     wait, read, release) a K-block of 128 pays for, 0.76 us each, twice its MMAs;
+//   * 4096 rows of 32 experts of 4096 x 6144 bf16 301 us (weights alone 245 at a
+//     copy's rate), 8192 rows back to their gradient 376;
+//   * weight gradients of 16384 rows of the same experts 1050 us in fp32 (3.2 GB
+//     written: 490 at a copy's rate), 870 in bf16: loads and stores without MMAs
+//     take 1010, the stores' and loads' turns on the memory's bus;
+//   * one token's eight experts: bf16 69 us (5.85 TB/s), e4m3 42 (4.8 TB/s): the
+//     weights' stream, and its start and end.
+//
+// Tiles: whole waves of tiles are dealt to the workers in order; the tiles of the
+// last, incomplete wave, where that pays, as one sequence of K-blocks, cut into
+// equal ranges, so few tiles (one token's experts) still use every SM.  A tile cut
 // by a range's end leaves fp32 partial sums in the workspace; the CTA that
 // finishes last adds them in the order of the ranges (the same bits whoever
 // is last) and writes the tile.
@@ -66,7 +84,7 @@ constexpr int kSmemMax = 227 * 1024;
 // where a whole tile costs a worker at most Cfg::kCutCost K-blocks more than its
 // range.
 constexpr int kMinRange = 12;
-constexpr int kBand = 8;
+constexpr int kBand = 8;               // row tiles that share their weights' strips in L2
 // kDw: a warp's stores leave through kStoreBufs stagings of 32 rows x 64 bytes
 constexpr int kStoreBytes = 32 * 64, kStoreBufs = 3;
 
@@ -103,16 +121,16 @@ struct Cfg {
     static constexpr int BK = FP8 ? 128 : 64;              // reduction per stage
     static constexpr bool kRows = MODE == kFwdRows;
     // A part of B is loaded by one tensor copy of its rows rounded up to this: a
-    // box of 1 .. kBoxes times as many rows (each copy costs the loading thread
-    // about 25 ns: with boxes of 32 rows alone 8192 x 6144 x 6144 took 4 % longer).
+    // box of 1 .. kBoxes times as many rows (with several copies of 32 rows 8192 x
+    // 6144 x 6144 took 4 % longer).
     static constexpr int kBoxRows = kRows ? 128 : BN == 256 ? 32 : 16;
-    static constexpr int kBoxes = MODE == kDw ? 0 : BN / CTAS / kBoxRows;
+    [[maybe_unused]] static constexpr int kBoxes = MODE == kDw ? 0 : BN / CTAS / kBoxRows;
     static constexpr int kBBytes = BN / CTAS * kRowBytes;
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr bool kColScale = FP8 && MODE != kFwdRows;  // scales per column
     // Accumulators per handover: a narrow e4m3 tile's K-block is little work, and
     // the round trip of its accumulator, paid for each, took 0.53 us of a K-block
-    // whose weights come in 0.2.
+    // whose weights come in 0.2 (one token's eight experts 52 us, with four 42).
     static constexpr int kBatch = kColScale ? 4 : 1;
     static constexpr int kBufs = kTmemAll / (BN * kBatch);      // handovers under way
     // What partial sums cost, in K-blocks: a narrow tile's are 32 KB a CTA, a wide

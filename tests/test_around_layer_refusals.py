@@ -147,3 +147,29 @@ def test_binding_refuses_host_tensors_and_nothing():
     with pytest.raises(ValueError):
         c.coli_moe_block_norm_backward(0, 64, None, None, None, None, None, None, 0, 1.0, None, 1e-5,
                                        None, None, None, None, None)
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """They would reach the library as other numbers (2^32 + 2 rows as 2)."""
+    c, _ = _lib()
+    t, w, big = torch.zeros(2, 64), torch.zeros(64), 2 ** 32 + 2
+    with pytest.raises(ValueError, match="32 bits"):
+        c.coli_moe_block_norm(big, 64, t, None, None, None, c.COLI_GATE_NONE, 1.0, w, 1e-5, t, None)
+    with pytest.raises(ValueError, match="32 bits"):
+        c.coli_moe_block_norm_backward(big, 64, t, None, t, None, None, None, c.COLI_GATE_NONE, 1.0,
+                                       w, 1e-5, t, None, w, None, None)
+    with pytest.raises(ValueError, match="32 bits"):
+        c.coli_moe_block_norm_workspace_size(big, 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        c.coli_moe_grouped_workspace_size(big, 64)
+    for f in (c.coli_moe_grouped_mm, c.coli_moe_grouped_mm_dx):
+        with pytest.raises(ValueError, match="32 bits"):
+            f(big, 1, 64, 64, t, t, w, t, w)
+    with pytest.raises(ValueError, match="32 bits"):
+        c.coli_moe_grouped_mm_dw(2, 1, big, 64, t, t, w, t, False, w)
+    with pytest.raises(ValueError, match="32 bits"):
+        c.coli_moe_fp8_quantize_rows(big, 64, t, t, w)
+    with pytest.raises(ValueError, match="32 bits"):
+        c.coli_moe_fp8_grouped_mm(2, 1, 64, big, t, w, t, w, w, t, w)
+    with pytest.raises(TypeError):
+        c._ws_arg("workspace", 0)
