@@ -311,3 +311,71 @@ def test_binding_checks_sizes_types_and_layout():
     assert c.coli_moe_grouped_mm(R, E, 60, K, xb, torch.zeros(E, 60, K, device="cuda",
                                  dtype=torch.bfloat16), off, torch.empty(R, 60, device="cuda"), ws,
                                  raise_on_error=False) == c.COLI_ERR_SHAPE
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured one after the other with one workspace (cut tiles' partial sums,
+    counters, column sums), replayed in turn: the bits of the eager calls."""
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    R, E, N, K = 9, 4, 264, 2048
+    g = torch.Generator(device="cuda").manual_seed(21)
+    x, w, dy = (torch.randn(*s, generator=g, device="cuda").bfloat16()
+                for s in ((R, K), (E, N, K), (R, N)))
+    off = torch.tensor([0, 1, 5, 5, R], dtype=torch.int32, device="cuda")
+    ws = c.grouped_workspace(R, E)
+    out, dw = torch.empty(R, N, device="cuda"), torch.empty(E, N, K, device="cuda")
+
+    def forward():
+        c.coli_moe_grouped_mm(R, E, N, K, x, w, off, out, ws)
+
+    def backward():
+        c.coli_moe_grouped_mm_dw(R, E, N, K, dy, x, off, dw, False, ws)
+
+    forward(), backward()
+    want = out.clone(), dw.clone()
+    torch.cuda.synchronize()
+    graphs = []
+    for f in (forward, backward):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f()
+    for i in (0, 1, 1, 0, 0, 1):
+        (out, dw)[i].fill_(float("nan"))
+        graphs[i].replay()
+        assert torch.equal((out, dw)[i], want[i])
+    assert c.coli_moe_get_status(ws) == c.COLI_OK
+
+
+def test_two_host_threads():
+    """Calls from two threads on two streams, of kernels and widths that need
+    different amounts of shared memory."""
+    import threading
+
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    errors = []
+
+    def work(H, seed):
+        try:
+            T = 700
+            with torch.cuda.stream(torch.cuda.Stream()):
+                g = torch.Generator(device="cuda").manual_seed(seed)
+                x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+                pre = torch.ones(H, device="cuda")
+                o, want = torch.empty_like(x), None
+                for _ in range(100):
+                    c.coli_moe_block_norm(T, H, x, None, None, None, c.COLI_GATE_NONE, 1.0, pre,
+                                          1e-5, None, o)
+                    if want is None:
+                        want = o.clone()
+                    c.coli_moe_block_norm(T, H, x, x, None, None, c.COLI_GATE_NONE, 0.0, pre, 1e-5,
+                                          None, o)
+                    assert torch.equal(o, want)
+        except BaseException as e:  # noqa: BLE001 - handed to the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(H, i)) for i, H in enumerate((2048, 6144, 8192))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
