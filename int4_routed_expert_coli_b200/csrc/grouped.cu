@@ -1123,8 +1123,8 @@ coli_status launch_mm(const void* A, const void* B, MmArgs a, int N, int K, cuda
     constexpr int smem = fixed_smem<C>() + stage_count<C>() * C::kStage;
     static_assert(smem <= kSmemMax && stage_count<C>() >= 4, "shared memory");
     auto kernel = grouped_mm_kernel<MODE, FP8, BN, CTAS>;
-    static std::atomic<uint64_t> done;
-    if (allow_smem(reinterpret_cast<const void*>(kernel), smem, done) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess)
         return COLI_ERR_CUDA;
     const int grid = std::max(CTAS, std::min(sms, kMaxGrid) / CTAS * CTAS);
     cudaLaunchConfig_t cfg = {};

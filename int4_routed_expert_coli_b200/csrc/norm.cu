@@ -947,8 +947,8 @@ bool plan_ring(bool backward, const NormArgs& a, const void* const (&src)[4],
     // threads that the register file holds: 74 registers each, 128 backward
     const int resident = backward ? 512 : 768;
     for (int per_sm = std::max(1, std::min(3, resident / *threads)); per_sm >= 1; --per_sm) {
-        const int budget = (kRingSmem + 2048) / per_sm - 2048;
-        const int slots = std::min(7, (budget - (int)p->weights) / (int)p->slot);
+        const int room = (kRingSmem + 2048) / per_sm - 2048;
+        const int slots = std::min(7, (room - (int)p->weights) / (int)p->slot);
         // two rows in hand, one on its way; one CTA of very wide rows does with two
         if (slots < (per_sm == 1 ? 2 : 3)) continue;
         p->slots = slots;
@@ -966,9 +966,9 @@ cudaError_t launch_ring(bool backward, const NormArgs& a, const RingPlan& p, int
                         int smem, cudaStream_t st) {
     auto kernel = backward ? block_norm_bwd_ring_kernel<THREADS, XB, YB, OB>
                            : block_norm_ring_kernel<THREADS <= kRegThreads, XB, YB, OB>;
-    static std::atomic<uint64_t> done[2];
-    const cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), kRingSmem,
-                                       done[backward]);
+    // (always the same limit: host threads cannot lower it under each other)
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
     if (err != cudaSuccess) return err;
     return launch_serialized(kernel, dim3(grid), dim3(threads), smem, st, a, p);
 }
