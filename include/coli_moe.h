@@ -317,7 +317,8 @@ coli_status coli_moe_block_norm(int32_t T, int32_t H, const void *x, coli_out_dt
  *          call); zeros when T == 0 (dgate: [H])
  *   ws     needed for dpre_w, dpost_w and a channel gate's dgate: at least
  *          coli_moe_block_norm_workspace_size(T, H) bytes, 256-byte aligned
- *          (needs no clear)
+ *          (needs no clear).  The size never falls as T or H grows, so one
+ *          workspace serves all calls up to the T and H it was sized for.
  * Errors: as the forward call; INVALID_ARG also for a gradient of something
  * the call does not have; WORKSPACE. */
 size_t coli_moe_block_norm_workspace_size(int32_t T, int32_t H);

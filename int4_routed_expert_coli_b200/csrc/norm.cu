@@ -912,9 +912,20 @@ coli_status check_norm(int32_t T, int32_t H, int32_t gate_kind, const void* gate
     return COLI_OK;
 }
 
-// CTAs of the backward kernels, at most (each leaves one partial row of column
-// sums in the workspace).
-int norm_bwd_ctas(int T, int H) { return std::max(1, std::min(T, (H <= 512 ? 6 : 3) * 148)); }
+// CTAs of the backward kernels, at most (each leaves one partial row per column
+// sum in the workspace).  Narrow rows take more: 768, which keeps the workspace
+// within 1536 rows of H floats.  888 are 0.8 us faster where they make five rows a
+// CTA of six (4096 rows: 256 bf16 16.1 and 16.9, 500 fp32 17.1 and 18.0), 0.9 slower where
+// 768 do as many (1200 x 256 fp32 11.1 and 10.2, 2000 x 33 12.7 and 11.8).
+constexpr int kBwdNarrowH = 512, kBwdNarrowCtas = 768, kBwdCtas = 3 * 148;
+int norm_bwd_ctas(int T, int H) {
+    return std::max(1, std::min(T, H <= kBwdNarrowH ? kBwdNarrowCtas : kBwdCtas));
+}
+
+// Bytes that a call's partial rows take, behind the workspace's header.
+size_t norm_bwd_bytes(int T, int H) {
+    return sizeof(float) * 2 * (size_t)H * (size_t)norm_bwd_ctas(T, H);
+}
 
 // Where the ring kernels pay: enough values that the rows gain more than the
 // ring's start costs.  bf16, ring against one row a CTA, forward: 450 rows of 2048
@@ -1076,7 +1087,10 @@ coli_status coli_moe_block_norm(int32_t T, int32_t H, const void* x, coli_out_dt
 
 size_t coli_moe_block_norm_workspace_size(int32_t T, int32_t H) {
     if (T < 0 || H <= 0) return 0;
-    return kHeaderBytes + sizeof(float) * 2 * (size_t)H * (size_t)norm_bwd_ctas(T, H);
+    // never less than a narrower call's, whose rows have more CTAs: a workspace
+    // of some T and H serves every call with no more of either
+    return kHeaderBytes +
+           std::max(norm_bwd_bytes(T, H), norm_bwd_bytes(T, std::min(H, kBwdNarrowH)));
 }
 
 coli_status coli_moe_block_norm_backward(
@@ -1109,7 +1123,7 @@ coli_status coli_moe_block_norm_backward(
     if (columns) {
         if (!ws) return COLI_ERR_INVALID_ARG;
         if (!ptr_aligned(ws, 256)) return COLI_ERR_ALIGN;
-        if (ws_bytes < coli_moe_block_norm_workspace_size(T, H)) return COLI_ERR_WORKSPACE;
+        if (ws_bytes < kHeaderBytes + norm_bwd_bytes(T, H)) return COLI_ERR_WORKSPACE;
     }
     NormArgs a = {};
     a.T = T; a.H = H; a.y = y; a.post_w = post_w; a.gate = gate; a.pre_w = pre_w;

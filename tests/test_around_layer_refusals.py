@@ -173,3 +173,20 @@ def test_binding_refuses_sizes_past_32_bits():
         c.coli_moe_fp8_grouped_mm(2, 1, 64, big, t, w, t, w, w, t, w)
     with pytest.raises(TypeError):
         c._ws_arg("workspace", 0)
+
+
+def test_block_norm_workspace_serves_smaller_calls():
+    """The size grows with T and H, so a buffer for (T, H) holds every smaller
+    call; and it stays within 1536 rows of H floats behind the header."""
+    c, L = _lib()
+    size = L.coli_moe_block_norm_workspace_size
+    Ts = [1, 2, 148, 443, 444, 445, 739, 740, 741, 768, 769, 887, 888, 889, 1024, 4096, 1 << 24]
+    Hs = [1, 33, 64, 256, 505, 511, 512, 513, 520, 600, 852, 853, 854, 888, 1001, 6144, 16384]
+    for i, T in enumerate(Ts):
+        for j, H in enumerate(Hs):
+            n = size(T, H)
+            assert n <= c.COLI_WS_HEADER_BYTES + 4 * 1536 * H, (T, H, n)
+            if i:
+                assert n >= size(Ts[i - 1], H), (T, H)
+            if j:
+                assert n >= size(T, Hs[j - 1]), (T, H)

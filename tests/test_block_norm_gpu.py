@@ -332,3 +332,21 @@ def test_on_another_stream_and_replayed():
     assert torch.equal(s_out, want_s) and torch.equal(o, want_o)
     for k in got:
         assert torch.equal(got[k], want[k]), k
+
+
+def test_one_workspace_from_wide_to_narrow_rows():
+    """Sized once, for the widest call; narrow rows have more partial rows."""
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    T = 1100
+    ws = torch.full((c.coli_moe_block_norm_workspace_size(T, 600),), 255, dtype=torch.uint8,
+                    device="cuda")                      # (NaN as floats)
+    for H in (600, 513, 512, 505, 256, 36):
+        v = _inputs(T, H, torch.float32, torch.float32, True, "channel", seed=H)
+        ref, mag = _reference_backward(v, "channel")
+        got = {k: torch.empty(H, device="cuda") for k in ("dpre_w", "dpost_w", "dgate")}
+        c.coli_moe_block_norm_backward(
+            T, H, v["do"], v["ds"], v["x"], v["y"], v["post_w"], v["gate"], c.COLI_GATE_CHANNEL,
+            v["alpha"], v["pre_w"], EPS, None, None, got["dpre_w"], got["dpost_w"], got["dgate"], ws)
+        for k in got:
+            tol = U * ref[k].abs() + (256 + T + 16) * U * mag[k]
+            assert torch.all((got[k].double() - ref[k]).abs() <= tol), (H, k)
