@@ -417,6 +417,14 @@ coli_status coli_moe_profile_read(double *ms, int32_t *n_calls);
  * usable SMs than the handle saw): nothing is launched for it and the call
  * runs on the streaming kernels instead, with the same result. */
 #define COLI_INJECT_NOT_RESIDENT 2
+/* With COLI_INJECT_WITHHOLD_GROUPED the next grouped product (bf16 or 8-bit,
+ * any direction) never fills the first stage of its first block: the waits on
+ * it run out (a few seconds in all), the kernel ends, the status word reads
+ * COLI_ERR_TIMEOUT, that call's output is undefined and the workspace needs a
+ * clear.  With COLI_INJECT_SHORT_WAITS its waits give up after 5 ms instead of
+ * one second. */
+#define COLI_INJECT_WITHHOLD_GROUPED 3
+#define COLI_INJECT_SHORT_WAITS 4
 coli_status coli_moe_debug_inject(int32_t what);
 
 /* Static English text for a status code (never NULL). */

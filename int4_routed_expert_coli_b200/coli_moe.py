@@ -238,6 +238,8 @@ def coli_moe_get_status(ws, stream=None):
 
 COLI_INJECT_WITHHOLD_STAGE = 1
 COLI_INJECT_NOT_RESIDENT = 2
+COLI_INJECT_WITHHOLD_GROUPED = 3
+COLI_INJECT_SHORT_WAITS = 4
 
 
 def coli_moe_debug_inject(what: int):

@@ -12,6 +12,7 @@
 #include "decode.cuh"
 #include "handle.cuh"
 #include "prefill.cuh"
+#include "ptx.cuh"
 
 // Which kernels a call runs.  Up to 8 tokens with fewer routed pairs than
 // experts (T*k < E), the fused decode kernel; by default every other call the
@@ -102,6 +103,8 @@ struct ProfileState {
 };
 ProfileState g_prof;
 int g_withhold_item = -1;
+constexpr uint64_t kShortWaitNs = 5000000;  // COLI_INJECT_SHORT_WAITS
+coli::GroupedHook g_grouped_hook = {0, coli::kWaitLimitNs};
 
 void profile_begin_call(cudaStream_t st) {
     if (!g_prof.enabled) return;
@@ -200,6 +203,12 @@ int take_withhold_item() {
     return v;
 }
 
+GroupedHook take_grouped_hook() {
+    const GroupedHook v = g_grouped_hook;
+    if (v.withhold || v.wait_ns != kWaitLimitNs) g_grouped_hook = {0, kWaitLimitNs};
+    return v;
+}
+
 cudaEvent_t profile_event(int i) {
     if (!g_prof.enabled || g_prof.open_call < 0 || i < 0 || i > 4) return nullptr;
     return g_prof.events[(size_t)g_prof.open_call * 5 + i];
@@ -211,11 +220,20 @@ extern "C" {
 coli_status coli_moe_debug_inject(int32_t what) {
     if (what == 0) {
         g_withhold_item = -1;
+        g_grouped_hook = {0, coli::kWaitLimitNs};
         coli::decode_force_not_resident(false);
         return COLI_OK;
     }
     if (what == COLI_INJECT_WITHHOLD_STAGE) {
         g_withhold_item = 0;  // the first item of CTA 0: a shared-expert gate/up tile
+        return COLI_OK;
+    }
+    if (what == COLI_INJECT_WITHHOLD_GROUPED) {
+        g_grouped_hook.withhold = 1;
+        return COLI_OK;
+    }
+    if (what == COLI_INJECT_SHORT_WAITS) {
+        g_grouped_hook.wait_ns = kShortWaitNs;
         return COLI_OK;
     }
     if (what == COLI_INJECT_NOT_RESIDENT) {

@@ -17,7 +17,8 @@ constexpr int kMaxTopK = 32;      // k limit (one route lane per slot)
 constexpr int kMaxShared = 4;
 constexpr size_t kHeaderBytes = 16384; // status word + tile counters at the start of ws
 constexpr size_t kSlotCntOffset = 1024; // int counters: finished gate/up items per expert slot
-constexpr size_t kTileCntOffset = 8192; // int counters: finished down items per 32-row tile
+constexpr size_t kTileCntOffset = 8192; // int counters: finished down items per 32-row tile;
+                                        // grouped products: cut tiles' finished ranges
 constexpr size_t kBatchCntOffset = 64;  // 2 int counters: tiles handed out by the small-batch
                                         // gate/up and down kernels (zeroed by the preparation)
 constexpr int kSmallT = 64;            // calls with T <= kSmallT use the fused prep kernel
@@ -158,6 +159,13 @@ inline void profile_mark(int i, cudaStream_t st) {
 // Test hook (coli_moe_debug_inject): item index the next FFN launch's producer
 // withholds, or -1.  Reading it clears it.
 int take_withhold_item();
+// Test hooks of the next grouped product: CTA 0's first stage withheld, and the
+// time limit of its waits.  Reading them clears them.
+struct GroupedHook {
+    int withhold;
+    uint64_t wait_ns;
+};
+GroupedHook take_grouped_hook();
 
 // ---- launchers (each returns cudaGetLastError() of its launch) ----------
 cudaError_t launch_router_logits(int T, int E, int H, const __nv_bfloat16* x, const float* wr,

@@ -45,12 +45,14 @@
 // Tiles: whole waves of tiles are dealt to the workers in order; the tiles of the
 // last, incomplete wave, where that pays, as one sequence of K-blocks, cut into
 // equal ranges, so few tiles (one token's experts) still use every SM.  A tile cut
-// by a range's end leaves fp32 partial sums in the workspace; the CTA that
-// finishes last adds them in the order of the ranges (the same bits whoever
-// is last) and writes the tile.
+// by a range's end leaves fp32 partial sums in the workspace; of the warps that
+// hold the same part of a tile, the one that finishes last adds them in the order
+// of the ranges (the same bits whoever is last) and writes it.
 //
 // Rows before offsets[0] and behind offsets[E] are neither read into a result
-// nor written.  Every wait is bounded (COLI_ERR_TIMEOUT).
+// nor written.  Every wait is bounded (COLI_ERR_TIMEOUT): the roles of a CTA wait
+// for each other at barriers in shared memory only, with a limit, and meet once,
+// at the kernel's end, which each reaches when its own next wait runs out.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -108,8 +110,10 @@ struct MmArgs {
     const float* xs;      // fp8: [KB][R] scales of the rows
     const float* ws;      // fp8: [E][ceil(M/128)][KB] scales of the weights
     float* part;          // partial tiles, two per CTA
-    int* counters;        // one per CTA, zero between calls
+    int* counters;        // one per epilogue warp, zero between calls
     int* status;
+    uint64_t wait_ns;     // time limit of a wait
+    int withhold;         // test hook: CTA 0's first stage never fills
 };
 
 // CTAS = 2: a pair of CTAs works on one tile of 256 M rows.  Each holds its
@@ -168,7 +172,6 @@ struct Shared {
     uint64_t tail_full[kMaxStages], tail_ready[kMaxStages];
     uint32_t tmem;
     int abort;
-    int last;                              // this CTA finishes the cut tile
     int kb_max;                            // K-blocks of the longest tile
     int whole, wave, range;                // whole tiles; steps of the last wave, of a range of it
     long long base;                        // first step of the last wave
@@ -399,7 +402,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&s.full[i], 1);
+            // (an arrival that never comes withholds the stage)
+            mbar_init(&s.full[i], i == 0 && blockIdx.x == 0 && a.withhold ? 2 : 1);
             mbar_init(&s.empty[i], 1);
             mbar_init(&s.tail_full[i], 1);
             mbar_init(&s.tail_ready[i], CTAS);
@@ -498,6 +502,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
         report(a.status, COLI_ERR_TIMEOUT);
         *abort = 1;
     };
+    // one answer for a whole warp
+    auto warp_aborted = [&]() { return __shfl_sync(0xffffffffu, (int)*abort, 0) != 0; };
     Walk<MODE, C> walk(a, s);
     Piece p = {};
 
@@ -538,7 +544,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     bool ok = true;
                     int k = p.kb0 * C::BK;
                     for (int kb = p.kb0; kb < p.kb1; ++kb, k += C::BK) {
-                        if (!tc::wait(empty0 + stage * 8, free)) {
+                        if (!tc::wait(empty0 + stage * 8, free, a.wait_ns)) {
                             timeout();
                             ok = false;
                             break;
@@ -605,9 +611,9 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                 if (*abort) {
                     if (rank == 0)
                         for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-                            tc::wait(&s.full[j % kStages], (j / kStages) & 1);
+                            tc::wait(full0 + j % kStages * 8, (j / kStages) & 1, a.wait_ns);
                     if (last_tail >= 0)
-                        tc::wait(&s.tail_full[last_tail], (tails >> last_tail & 1) ^ 1);
+                        tc::wait(tail0 + last_tail * 8, (tails >> last_tail & 1) ^ 1, a.wait_ns);
                 }
             }
         } else if (warp == 1) {
@@ -646,17 +652,18 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     bool ok = true;
                     for (int c0 = p.kb0; c0 < p.kb1 && ok; c0 += len) {
                         const int c1 = min(c0 + len, p.kb1);
-                        ok = tc::wait(aempty0 + buf * 8, drained);
+                        ok = tc::wait(aempty0 + buf * 8, drained, a.wait_ns);
                         for (int kb = c0; kb < c1 && ok; ++kb) {
                             const uint32_t d =
                                 tmem + (buf * C::kBatch + (C::kBatch > 1 ? kb - c0 : 0)) * C::BN;
-                            ok = tc::wait(full0 + stage * 8, full);
+                            ok = tc::wait(full0 + stage * 8, full, a.wait_ns);
                             const uint64_t ad = ad0 + stage * (C::kStage / 16);
                             const uint64_t bd = bd0 + stage * (C::kStage / 16);
                             if (MODE == kDw && p.rows - kb * C::BK < C::BK) {
                                 // a group's cut last K-block: whole MMA steps behind its
                                 // end are left out, warp 2 clears the rest of the last
-                                ok = ok && tc::wait_cluster(ready0 + stage * 8, tails >> stage & 1);
+                                ok = ok && tc::wait_cluster(ready0 + stage * 8,
+                                                            tails >> stage & 1, a.wait_ns);
                                 tails ^= 1u << stage;
                                 tc::fence_after();
                                 const int steps = (p.rows - kb * C::BK + 15) / 16;
@@ -695,14 +702,14 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
             // (rows of the next group, in both operands: they may hold infinities), up
             // to the next MMA step.  In a pair each CTA clears its own part.
             uint32_t it = 0, tails = 0;
-            while (!*abort && walk.next(p)) {
+            while (!warp_aborted() && walk.next(p)) {
                 if (p.rows == 0) continue;
                 it += p.kb1 - p.kb0;
                 const int valid = p.rows - (p.kb1 - 1) * C::BK;
                 if (valid >= C::BK) continue;
                 const int i = (it - 1) % kStages;
-                if (!tc::wait(&s.tail_full[i], tails >> i & 1)) {
-                    timeout();
+                if (!tc::wait_warp(&s.tail_full[i], tails >> i & 1, a.wait_ns)) {
+                    if (lane == 0) timeout();
                     break;
                 }
                 tails ^= 1u << i;
@@ -731,7 +738,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                 const int KB = (a.red + C::BK - 1) / C::BK;
                 const int w_tiles = (a.M + kBM - 1) / kBM;
                 uint32_t ch = 0;
-                while (!*abort && walk.next(p)) {
+                while (!warp_aborted() && walk.next(p)) {
                     // (an odd CTA past the last weight rows computes nothing that is stored)
                     const int wt = min(p.m0 / kBM, w_tiles - 1);
                     const float* wsc = a.ws + ((int64_t)p.e * w_tiles + wt) * KB + p.kb0;
@@ -739,7 +746,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     bool ok = true;
                     for (int k0 = p.kb0; k0 < p.kb1; k0 += C::kBatch, ++ch) {
                         const uint32_t b = ch % kScaleBufs;
-                        if (!tc::wait(&s.sc_empty[b], (ch / kScaleBufs & 1) ^ 1)) {
+                        if (!tc::wait_warp(&s.sc_empty[b], (ch / kScaleBufs & 1) ^ 1, a.wait_ns)) {
                             if (lane == 0) timeout();
                             ok = false;
                             break;
@@ -769,7 +776,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
         const uint32_t acc_empty =
             CTAS == 2 ? tc::cluster_addr(&s.acc_empty[0], 0) : smem_addr(&s.acc_empty[0]);
         uint32_t ch = 0;
-        while (!*abort && walk.next(p)) {
+        while (!warp_aborted() && walk.next(p)) {
             // the two warps of a lane quarter share the columns evenly
             // (kFwdRows: the columns of one weight scale each)
             const int hn = C::kRows ? 128 : (p.n + 63) / 64 * 32;
@@ -817,8 +824,9 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                         const float2 f = ring[(i & (kScaleRing - 1)) * (kEpiWarps * 32)];
                         one = f.x * f.y;
                     }
-                    if (!tc::wait(&s.acc_full[buf], (ch / C::kBufs) & 1) ||
-                        (C::kColScale && !tc::wait(&s.sc_full[sb], (ch / kScaleBufs) & 1))) {
+                    if (!tc::wait_warp(&s.acc_full[buf], (ch / C::kBufs) & 1, a.wait_ns) ||
+                        (C::kColScale &&
+                         !tc::wait_warp(&s.sc_full[sb], (ch / kScaleBufs) & 1, a.wait_ns))) {
                         if (lane == 0) timeout();
                         ok = false;
                         break;
@@ -858,7 +866,9 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
 
             if (p.kb1 - p.kb0 < p.kb) {
                 // a cut tile: leave the partial sums; the last of its ranges adds
-                // them, in the order of the ranges
+                // them, in the order of the ranges.  Each warp reads only what the
+                // same warp of another CTA left, so it counts and goes on by itself.
+                if (nc == 0) continue;
                 const int c_first = p.step / s.range;
                 const int c_last = (p.step + p.kb - 1) / s.range;
                 constexpr int kPart = kBM * C::BN;
@@ -871,14 +881,14 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                 for (int j = 0; j < C::kAcc; ++j)
                     if (j < nc) __stcg(mine + j * kBM, acc[j]);
                 __threadfence();
-                named_barrier(1, kEpiWarps * 32);
-                if (warp == C::kFront && lane == 0) {
-                    int* count = a.counters + c_first * CTAS + rank;
-                    s.last = atomicAdd(count, 1) == c_last - c_first;
-                    if (s.last) *count = 0;
+                __syncwarp();
+                int last = 0;
+                if (lane == 0) {
+                    int* count = a.counters + (c_first * CTAS + rank) * kEpiWarps + warp - C::kFront;
+                    last = atomicAdd(count, 1) == c_last - c_first;
+                    if (last) *count = 0;
                 }
-                named_barrier(1, kEpiWarps * 32);
-                if (!*const_cast<volatile int*>(&s.last)) continue;
+                if (!__shfl_sync(0xffffffffu, last, 0)) continue;
                 __threadfence();
 #pragma unroll
                 for (int j = 0; j < C::kAcc; ++j) acc[j] = 0.f;
@@ -1159,6 +1169,7 @@ bool narrow(int R, int E, int M) {
     return (int64_t)R <= 48 * (int64_t)E + 16 || rows * ((M + kBM - 1) / kBM) <= 64 * 160;
 }
 
+static_assert(sizeof(int) * kMaxGrid * kEpiWarps <= kHeaderBytes - kTileCntOffset, "counters");
 constexpr size_t kPartBytes = sizeof(float) * kMaxGrid * 2 * kBM * 256;
 
 coli_status check_mm(int32_t R, int32_t E, int32_t N, int32_t K, int grain) {
@@ -1193,6 +1204,9 @@ MmArgs make_mm_args(const int32_t* offsets, int R, int E, int M, int red, void* 
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kHeaderBytes);
     a.counters = reinterpret_cast<int*>(static_cast<char*>(ws) + kTileCntOffset);
     a.status = static_cast<int*>(ws);
+    const GroupedHook hook = take_grouped_hook();
+    a.wait_ns = hook.wait_ns;
+    a.withhold = hook.withhold;
     return a;
 }
 

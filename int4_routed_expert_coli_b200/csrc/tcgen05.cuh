@@ -234,7 +234,7 @@ __device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
-// Bounded waits for a phase, false after kWaitLimitNs.  A try suspends the
+// Bounded waits for a phase, false after `limit` ns.  A try suspends the
 // thread until the phase completes or kTryNs have passed: threads that poll take
 // issue slots from the two that feed the tensor cores (8192 x 6144 x 6144 bf16
 // took 434 us with plain tries, 404 us so).
@@ -263,21 +263,30 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint64_t limit) {
     if (try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (!try_wait(bar, parity))
-        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+        if (global_timer_ns() - t0 > limit) return false;
     return true;
 }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-    return wait(smem_addr(bar), parity);
+// A whole warp's wait: its lanes go on or leave together.  A phase that this warp
+// must still release stays complete, so lanes can differ only over the limit, and
+// those that get there vote.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit) {
+    const uint32_t at = smem_addr(bar);
+    if (try_wait(at, parity)) return true;
+    const unsigned lanes = __activemask();
+    const uint64_t t0 = global_timer_ns();
+    while (!__any_sync(lanes, try_wait(at, parity)))
+        if (__any_sync(lanes, global_timer_ns() - t0 > limit)) return false;
+    return true;
 }
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit) {
     if (try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (!try_wait_cluster(bar, parity))
-        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+        if (global_timer_ns() - t0 > limit) return false;
     return true;
 }
 

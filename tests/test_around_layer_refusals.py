@@ -190,3 +190,16 @@ def test_block_norm_workspace_serves_smaller_calls():
                 assert n >= size(Ts[i - 1], H), (T, H)
             if j:
                 assert n >= size(T, Hs[j - 1]), (T, H)
+
+
+def test_grouped_fault_hooks_match_the_header():
+    import os
+    import re
+    c, L = _lib()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = open(os.path.join(root, "include", "coli_moe.h")).read()
+    for name in ("COLI_INJECT_WITHHOLD_GROUPED", "COLI_INJECT_SHORT_WAITS"):
+        m = re.search(r"#define\s+" + name + r"\s+(\d+)", src)
+        assert m and int(m.group(1)) == getattr(c, name)
+        assert L.coli_moe_debug_inject(getattr(c, name)) == c.COLI_OK
+    assert L.coli_moe_debug_inject(0) == c.COLI_OK

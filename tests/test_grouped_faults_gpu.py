@@ -1,0 +1,73 @@
+"""The grouped products' bounded waits, without faulting the GPU: a stage that
+is never filled makes the waits of every role run out; the kernel ends, the
+status word reads COLI_ERR_TIMEOUT, and after a clear the same call gives the
+same bits as before."""
+import pytest
+import torch
+
+from gpu_util import requires_gpu
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+
+
+def _rn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+
+def _call(c, op, counts, N, K, ws, seed=0):
+    """One call of `op`; returns a function that makes it into a new output."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    E, R = len(counts), sum(counts)
+    off = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32,
+                       device="cuda")
+    x, dy, w = _rn(g, R, K), _rn(g, R, N), _rn(g, E, N, K)
+
+    def run():
+        shape = {"mm": (R, N), "fp8": (R, N), "dx": (R, K), "dw": (E, N, K)}[op]
+        out = torch.zeros(shape, device="cuda")
+        if op == "mm":
+            c.coli_moe_grouped_mm(R, E, N, K, x, w, off, out, ws)
+        elif op == "dx":
+            c.coli_moe_grouped_mm_dx(R, E, N, K, dy, w, off, out, ws)
+        elif op == "dw":
+            c.coli_moe_grouped_mm_dw(R, E, N, K, dy, x, off, out, False, ws)
+        else:
+            kb = -(-K // 128)
+            xq = torch.empty(R, K, dtype=torch.float8_e4m3fn, device="cuda")
+            xs = torch.empty(kb, R, device="cuda")
+            c.coli_moe_fp8_quantize_rows(R, K, x, xq, xs)
+            wq = w.to(torch.float8_e4m3fn)
+            sw = torch.full((E, -(-N // 128), kb), 0.25, device="cuda")
+            c.coli_moe_fp8_grouped_mm(R, E, N, K, xq, xs, wq, sw, off, out, ws)
+        return out
+    return run
+
+
+# narrow and wide tiles, whole and cut (a cut tile's partial sums are added by
+# whoever finishes last), one CTA and pairs, e4m3 with the weights and the rows as M
+@pytest.mark.parametrize("op,counts,N,K", [
+    ("mm", [1] * 8 + [0] * 24, 512, 4096),
+    ("mm", [3000], 520, 200),
+    ("mm", [513], 2312, 6144),
+    ("dx", [8], 4096, 6144),
+    ("dw", [37, 3, 60], 128, 192),
+    ("dw", [16371], 512, 512),
+    ("fp8", [1] * 8, 512, 6144),
+    ("fp8", [513], 2312, 6144),
+])
+def test_withheld_stage_times_out_and_the_next_call_is_right(op, counts, N, K):
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    ws = c.grouped_workspace(sum(counts), len(counts))
+    run = _call(c, op, counts, N, K, ws)
+    want = run()
+    assert c.coli_moe_get_status(ws) == c.COLI_OK
+    assert c.coli_moe_debug_inject(c.COLI_INJECT_WITHHOLD_GROUPED) == c.COLI_OK
+    try:
+        run()
+    finally:
+        c.coli_moe_debug_inject(0)
+    assert c.coli_moe_get_status(ws) == c.COLI_ERR_TIMEOUT
+    c.coli_moe_workspace_clear(ws)
+    got = run()
+    assert c.coli_moe_get_status(ws) == c.COLI_OK
+    assert torch.equal(got, want)
