@@ -82,6 +82,7 @@ constexpr int kChunk = 12;             // bf16 K-blocks per accumulator chain, a
 constexpr int kScaleBufs = 4;          // handovers whose column scales are loaded ahead
 constexpr int kScaleRing = 8;          // kFwdRows: K-blocks whose scales are loaded ahead
 constexpr int kSmemMax = 227 * 1024;
+constexpr uint64_t kSettleNs = 100000; // after a timeout, for copies that no barrier counts
 // The last wave is cut into ranges of kMinRange K-blocks at least, and not at all
 // where a whole tile costs a worker at most Cfg::kCutCost K-blocks more than its
 // range.
@@ -170,6 +171,7 @@ struct Shared {
     // kDw, a group's cut last K-block: its copies are done; the rows behind the
     // group's end are cleared
     uint64_t tail_full[kMaxStages], tail_ready[kMaxStages];
+    uint64_t mma_done;                     // after a timeout: no MMA is under way
     uint32_t tmem;
     int abort;
     int kb_max;                            // K-blocks of the longest tile
@@ -416,6 +418,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
             mbar_init(&s.sc_full[i], 32);  // one arrival per copying lane
             mbar_init(&s.sc_empty[i], kEpiWarps);
         }
+        mbar_init(&s.mma_done, 1);
         s.abort = 0;
         s.kb_max = MODE == kDw ? 0 : (a.red + C::BK - 1) / C::BK;
         fence_barrier_init();
@@ -605,15 +608,19 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     }
                     if (!ok) break;
                 }
-                // after a timeout nobody consumes the stages: the copies in flight
-                // still end before this CTA does (those of the odd CTA complete on
-                // the even one's barriers)
-                if (*abort) {
-                    if (rank == 0)
-                        for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-                            tc::wait(full0 + j % kStages * 8, (j / kStages) & 1, a.wait_ns);
-                    if (last_tail >= 0)
-                        tc::wait(tail0 + last_tail * 8, (tails >> last_tail & 1) ^ 1, a.wait_ns);
+                // Whoever consumes the stages may give up at any time: the copies in
+                // flight end before this CTA does (those of the odd CTA complete on
+                // the even one's barriers, and a pair ends together).
+                if (rank == 0)
+                    for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+                        tc::wait(full0 + j % kStages * 8, (j / kStages) & 1, a.wait_ns);
+                if (last_tail >= 0)
+                    tc::wait(tail0 + last_tail * 8, (tails >> last_tail & 1) ^ 1, a.wait_ns);
+                if (CTAS == 2 && *abort) {
+                    // the other CTA may have filled a stage that this one did not
+                    // arm: time enough for a stage's copies to land
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < kSettleNs) __nanosleep(1000);
                 }
             }
         } else if (warp == 1) {
@@ -664,13 +671,15 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                                 // end are left out, warp 2 clears the rest of the last
                                 ok = ok && tc::wait_cluster(ready0 + stage * 8,
                                                             tails >> stage & 1, a.wait_ns);
+                                if (!ok) break;
                                 tails ^= 1u << stage;
                                 tc::fence_after();
                                 const int steps = (p.rows - kb * C::BK + 15) / 16;
-                                for (int k = 0; k < steps && ok; ++k)
+                                for (int k = 0; k < steps; ++k)
                                     tc::mma<FP8, CTAS>(d, ad + k * kAStep, bd + k * kBStep, id,
                                                        kb > c0 || k > 0);
-                            } else if (ok) {
+                            } else {
+                                if (!ok) break;
                                 tc::fence_after();
                                 tc::mma<FP8, CTAS>(d, ad, bd, id, !FP8 && kb > c0);
 #pragma unroll
@@ -683,6 +692,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                                 full ^= 1;
                             }
                         }
+                        if (!ok) break;  // (no stage or accumulator of a failed wait is passed on)
                         tc::commit<CTAS>(afull0 + buf * 8);
                         buf = buf + 1 == C::kBufs ? 0 : buf + 1;
                         drained ^= buf == 0;
@@ -695,6 +705,12 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                         timeout();
                         break;
                     }
+                }
+                // after a timeout nobody waits for the last MMAs: they end before
+                // tensor memory is freed
+                if (*abort) {
+                    tc::commit_here<CTAS>(smem_addr(&s.mma_done));
+                    tc::wait(smem_addr(&s.mma_done), 0, a.wait_ns);
                 }
             }
         } else if (MODE == kDw && warp == 2) {
@@ -1029,6 +1045,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
             __syncwarp();
         }
         if (MODE == kDw && lane == 0) tc::store_wait();
+        if constexpr (C::kRows) tc::cp_async_wait<0>();
     }
 
     __syncwarp();

@@ -69,6 +69,16 @@ __device__ __forceinline__ void commit(uint32_t bar) {
             : "memory");
 }
 
+// The same on this CTA's barrier alone.
+template <int CTAS>
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+    if constexpr (CTAS == 1) commit<1>(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+            : "memory");
+}
+
 template <int CTAS>
 __device__ __forceinline__ void alloc(uint32_t* slot, uint32_t cols) {
     if constexpr (CTAS == 1) {

@@ -71,3 +71,27 @@ def test_withheld_stage_times_out_and_the_next_call_is_right(op, counts, N, K):
     got = run()
     assert c.coli_moe_get_status(ws) == c.COLI_OK
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("op,counts,N,K", [("mm", [700], 2312, 6144), ("dw", [3000, 37], 512, 512),
+                                           ("fp8", [700], 2312, 6144)])
+def test_a_call_that_gave_up_leaves_the_next_one_alone(op, counts, N, K):
+    """Its copies and MMAs in flight end with it: calls that follow at once, on a
+    workspace of their own, start on its SMs and are right."""
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    R, E = sum(counts), len(counts)
+    bad, ws = c.grouped_workspace(R, E), c.grouped_workspace(R, E)
+    first, run = _call(c, op, counts, N, K, bad, seed=1), _call(c, op, counts, N, K, ws)
+    want = run()
+    torch.cuda.synchronize()
+    assert c.coli_moe_debug_inject(c.COLI_INJECT_SHORT_WAITS) == c.COLI_OK
+    assert c.coli_moe_debug_inject(c.COLI_INJECT_WITHHOLD_GROUPED) == c.COLI_OK
+    try:
+        first()
+    finally:
+        c.coli_moe_debug_inject(0)
+    got = [run() for _ in range(4)]
+    assert c.coli_moe_get_status(bad) == c.COLI_ERR_TIMEOUT
+    assert c.coli_moe_get_status(ws) == c.COLI_OK
+    for t in got:
+        assert torch.equal(t, want)
