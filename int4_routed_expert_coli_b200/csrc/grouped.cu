@@ -173,6 +173,7 @@ struct Shared {
     uint64_t tail_full[kMaxStages], tail_ready[kMaxStages];
     uint64_t mma_done;                     // after a timeout: no MMA is under way
     uint32_t tmem;
+    uint32_t loaded;                       // kDw: K-blocks loaded so far
     int abort;
     int kb_max;                            // K-blocks of the longest tile
     int whole, wave, range;                // whole tiles; steps of the last wave, of a range of it
@@ -419,6 +420,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
             mbar_init(&s.sc_empty[i], kEpiWarps);
         }
         mbar_init(&s.mma_done, 1);
+        s.loaded = 0;
         s.abort = 0;
         s.kb_max = MODE == kDw ? 0 : (a.red + C::BK - 1) / C::BK;
         fence_barrier_init();
@@ -601,6 +603,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                                 tc::tma_2d<CTAS>(sb, bmap, k, p.row0 + b0, bar);
                         }
                         ++it;
+                        if (MODE == kDw) *const_cast<volatile uint32_t*>(&s.loaded) = it;
                         if (++stage == kStages) {
                             stage = 0;
                             free ^= 1;
@@ -716,7 +719,9 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
         } else if (MODE == kDw && warp == 2) {
             // ------ kDw: clear what lies behind a group's end in its last K-block ------
             // (rows of the next group, in both operands: they may hold infinities), up
-            // to the next MMA step.  In a pair each CTA clears its own part.
+            // to the next MMA step.  In a pair each CTA clears its own part.  Groups of
+            // whole K-blocks need none, so a wait can span the work of many tiles: its
+            // limit starts again whenever the loads go on.
             uint32_t it = 0, tails = 0;
             while (!warp_aborted() && walk.next(p)) {
                 if (p.rows == 0) continue;
@@ -724,7 +729,15 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                 const int valid = p.rows - (p.kb1 - 1) * C::BK;
                 if (valid >= C::BK) continue;
                 const int i = (it - 1) % kStages;
-                if (!tc::wait_warp(&s.tail_full[i], tails >> i & 1, a.wait_ns)) {
+                bool ok = tc::wait_warp(&s.tail_full[i], tails >> i & 1, a.wait_ns);
+                for (uint32_t seen = 0; !ok;) {
+                    const uint32_t now = __shfl_sync(
+                        0xffffffffu, *const_cast<volatile uint32_t*>(&s.loaded), 0);
+                    if (now == seen || warp_aborted()) break;
+                    seen = now;
+                    ok = tc::wait_warp(&s.tail_full[i], tails >> i & 1, a.wait_ns);
+                }
+                if (!ok) {
                     if (lane == 0) timeout();
                     break;
                 }

@@ -95,3 +95,33 @@ def test_a_call_that_gave_up_leaves_the_next_one_alone(op, counts, N, K):
     assert c.coli_moe_get_status(ws) == c.COLI_OK
     for t in got:
         assert torch.equal(t, want)
+
+
+def test_work_longer_than_a_wait_is_no_timeout():
+    """A weight gradient whose first group, of whole K-blocks, takes several times
+    a wait's limit (2.6e5 rows of 8192 x 8192, about 25 ms, waits of 5 ms) before
+    the group whose last K-block is cut."""
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    counts, N, K = [1 << 18, 37], 8192, 8192
+    R, E = sum(counts), 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, dy = (torch.empty(R, 8192, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+             for _ in range(2))
+    off = torch.tensor([0, counts[0], R], dtype=torch.int32, device="cuda")
+    ws = c.grouped_workspace(R, E)
+    dw = [torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    c.coli_moe_grouped_mm_dw(R, E, N, K, dy, x, off, dw[0], False, ws)
+    assert c.coli_moe_get_status(ws) == c.COLI_OK
+    assert c.coli_moe_debug_inject(c.COLI_INJECT_SHORT_WAITS) == c.COLI_OK
+    try:
+        c.coli_moe_grouped_mm_dw(R, E, N, K, dy, x, off, dw[1], False, ws)
+    finally:
+        c.coli_moe_debug_inject(0)
+    assert c.coli_moe_get_status(ws) == c.COLI_OK
+    assert torch.equal(dw[0], dw[1])
+    rows, cols = slice(N - 8, N), slice(K - 8, K)
+    for e, r in ((0, slice(0, counts[0])), (1, slice(counts[0], R))):
+        ref = dy[r, rows].double().T @ x[r, cols].double()
+        mag = dy[r, rows].double().abs().T @ x[r, cols].double().abs()
+        tol = 2.0 ** -8 * ref.abs() + (counts[e] / 16 + 64) * 2.0 ** -23 * mag
+        assert torch.all((dw[0][e, rows, cols].double() - ref).abs() <= tol)
