@@ -174,6 +174,7 @@ struct Shared {
     uint64_t mma_done;                     // after a timeout: no MMA is under way
     uint32_t tmem;
     uint32_t loaded;                       // kDw: K-blocks loaded so far
+    int bad;                               // an offset pair is impossible
     int abort;
     int kb_max;                            // K-blocks of the longest tile
     int whole, wave, range;                // whole tiles; steps of the last wave, of a range of it
@@ -421,6 +422,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
         }
         mbar_init(&s.mma_done, 1);
         s.loaded = 0;
+        s.bad = 0;
         s.abort = 0;
         s.kb_max = MODE == kDw ? 0 : (a.red + C::BK - 1) / C::BK;
         fence_barrier_init();
@@ -437,6 +439,13 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
     // Tiles and K-block steps before each group (of one M tile): a scan over
     // the groups, kPer per thread.  An impossible offset pair is reported and
     // gets no tile.
+    auto group_tiles = [&](int rows) -> long long {
+        constexpr int kTileRows = Walk<MODE, C>::kTileRows;
+        return MODE == kDw ? 1 : (rows + kTileRows - 1) / kTileRows;
+    };
+    auto tile_kb = [&](int rows) {
+        return MODE == kDw ? max(1, (rows + C::BK - 1) / C::BK) : (a.red + C::BK - 1) / C::BK;
+    };
     {
         constexpr int kPer = (kMaxExperts + 1 + C::kThreads - 1) / C::kThreads;
         long long v[kPer], w[kPer], sum_v = 0, sum_w = 0;
@@ -450,14 +459,11 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                 if (e + 1 == a.E) s.off[e + 1] = hi;
                 if (lo < 0 || hi < lo || hi > a.R) {
                     report(a.status, COLI_ERR_BAD_INDEX);
-                } else if (MODE == kDw) {
-                    v[i] = 1;
-                    w[i] = max(1, (hi - lo + C::BK - 1) / C::BK);
-                    atomicMax(&s.kb_max, (int)w[i]);
+                    s.bad = 1;
                 } else {
-                    constexpr int kTileRows = Walk<MODE, C>::kTileRows;
-                    v[i] = (hi - lo + kTileRows - 1) / kTileRows;
-                    w[i] = v[i] * ((a.red + C::BK - 1) / C::BK);
+                    v[i] = group_tiles(hi - lo);
+                    w[i] = v[i] * tile_kb(hi - lo);
+                    if (MODE == kDw) atomicMax(&s.kb_max, (int)w[i]);
                 }
             }
             sum_v += v[i];
@@ -495,7 +501,27 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) Walk<MODE, C>::plan(a, s);
+    if (threadIdx.x == 0) {
+        // Behind a pair that descends, a group may start inside an earlier one: it
+        // gets no tile either, or both would write its rows.  (Rare enough for one
+        // thread.)
+        if (s.bad) {
+            long long tiles = 0, steps = 0;
+            int end = 0;
+            for (int e = 0; e < a.E; ++e) {
+                const int lo = s.off[e], hi = s.off[e + 1];
+                s.tile0[e] = (int)tiles;
+                s.step0[e] = steps;
+                if (lo < end || hi < lo || hi > a.R) continue;
+                end = hi;
+                tiles += group_tiles(hi - lo);
+                steps += group_tiles(hi - lo) * tile_kb(hi - lo);
+            }
+            s.tile0[a.E] = (int)tiles;
+            s.step0[a.E] = steps;
+        }
+        Walk<MODE, C>::plan(a, s);
+    }
     tc::fence_before();
     __syncthreads();
     if constexpr (CTAS == 2) tc::cluster_sync();  // the pair's barriers are ready

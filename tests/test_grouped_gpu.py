@@ -289,3 +289,51 @@ def test_repeats_bit_for_bit_and_replays():
     c.coli_moe_grouped_mm(R, E, N, K, x, w, off, out[0], ws)
     assert torch.equal(out[0], out[1])
     assert c.coli_moe_get_status(ws) == c.COLI_OK
+
+
+@pytest.mark.parametrize("offsets,kept", [
+    ([0, 10, 5, 10, 30], [(0, 0, 10), (3, 10, 30)]),
+    ([0, 20, 8, 30, 30, 40], [(0, 0, 20), (3, 30, 30), (4, 30, 40)]),
+    # [40, 90) leaves the rows; [50, 90) would too; [3, 12) is free of earlier groups
+    ([40, 90, 50, 90, 3, 12, 12, 2, 13, 20], [(4, 3, 12), (5, 12, 12), (8, 13, 20)]),
+])
+def test_groups_inside_an_earlier_one_are_skipped(offsets, kept):
+    """No row belongs to two groups, whatever the offsets: one that starts inside
+    an earlier group is left out like the pair that descends, and the same call
+    gives the same bits."""
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    E, R, N, K = len(offsets) - 1, 64, 264, 1040
+    g = _gen(11)
+    x, w, dy = _rn(g, R, K), _rn(g, E, N, K, scale=0.1), _rn(g, R, N)
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    ws = c.grouped_workspace(R, E)
+    wq = w.to(torch.float8_e4m3fn)
+    xq = torch.empty(R, K, dtype=torch.float8_e4m3fn, device="cuda")
+    sx = torch.empty(-(-K // 128), R, device="cuda")
+    c.coli_moe_fp8_quantize_rows(R, K, x, xq, sx)
+    sw = torch.ones(E, -(-N // 128), -(-K // 128), device="cuda")
+    X8 = xq.double() * sx.T.double().repeat_interleave(128, 1)[:, :K]
+    for repeat in range(2):
+        out, o8 = (torch.full((R, N), 7.0, device="cuda") for _ in range(2))
+        dx, dw = torch.full((R, K), 7.0, device="cuda"), torch.full((E, N, K), 7.0, device="cuda")
+        c.coli_moe_grouped_mm(R, E, N, K, x, w, off, out, ws)
+        c.coli_moe_grouped_mm_dx(R, E, N, K, dy, w, off, dx, ws)
+        c.coli_moe_grouped_mm_dw(R, E, N, K, dy, x, off, dw, False, ws)
+        c.coli_moe_fp8_grouped_mm(R, E, N, K, xq, sx, wq, sw, off, o8, ws)
+        assert c.coli_moe_get_status(ws) == c.COLI_ERR_BAD_INDEX
+        if repeat:
+            for a, b in zip(first, (out, dx, dw, o8)):
+                assert torch.equal(a, b)
+        first = out, dx, dw, o8
+    free = torch.ones(R, dtype=torch.bool, device="cuda")
+    for e, lo, hi in kept:
+        free[lo:hi] = False
+        X, W, D = x[lo:hi].double(), w[e].double(), dy[lo:hi].double()
+        _check(out[lo:hi], X @ W.T, X.abs() @ W.abs().T, K)
+        _check(dx[lo:hi], D @ W, D.abs() @ W.abs(), N)
+        _check(dw[e], D.T @ X, D.abs().T @ X.abs(), hi - lo)
+        W8 = wq[e].double()
+        _check(o8[lo:hi], X8[lo:hi] @ W8.T, X8[lo:hi].abs() @ W8.abs().T, K)
+    assert torch.all(out[free] == 7) and torch.all(dx[free] == 7) and torch.all(o8[free] == 7)
+    skipped = [e for e in range(E) if e not in [k[0] for k in kept]]
+    assert torch.all(dw[skipped] == 7)
