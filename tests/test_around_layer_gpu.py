@@ -379,3 +379,70 @@ def test_two_host_threads():
     for t in threads:
         t.join()
     assert not errors, errors
+
+
+def test_two_streams_and_graphs_with_cut_tiles():
+    """Products whose tiles are cut (partial sums in the workspace), the weight
+    gradient and the backward norm: on two streams at once, each with workspaces of
+    its own, and captured into two graphs that share workspaces, replayed in turn:
+    the bits of the eager calls."""
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    g = torch.Generator(device="cuda").manual_seed(31)
+    E, N, K, counts = 4, 264, 6144, [1, 4, 0, 4]
+    R, T, H = sum(counts), 300, 776
+    x, w, dy = _rn(g, R, K), _rn(g, E, N, K), _rn(g, R, N)
+    off = torch.tensor([0, 1, 5, 5, 9], dtype=torch.int32, device="cuda")
+    R2, n2 = 9003, 136
+    x2, dy2 = _rn(g, R2, n2), _rn(g, R2, n2)
+    off2 = torch.tensor([0, R2], dtype=torch.int32, device="cuda")
+    s, y, do = _rn(g, T, H), _rn(g, T, H), _rn(g, T, H)
+    pw, qw = torch.ones(H, device="cuda"), torch.ones(H, device="cuda")
+
+    class Set:
+        def __init__(self):
+            self.ws = c.grouped_workspace(R2, E)
+            self.ws[c.COLI_WS_HEADER_BYTES:].fill_(255)
+            self.nws = torch.empty(c.coli_moe_block_norm_workspace_size(T, H), dtype=torch.uint8,
+                                   device="cuda")
+            self.res = [torch.empty(R, N, device="cuda"), torch.empty(1, n2, n2, device="cuda"),
+                        torch.empty_like(s), torch.empty_like(y), torch.empty_like(pw),
+                        torch.empty_like(qw)]
+
+        def products(self):
+            c.coli_moe_grouped_mm(R, E, N, K, x, w, off, self.res[0], self.ws)
+            c.coli_moe_grouped_mm_dw(R2, 1, n2, n2, dy2, x2, off2, self.res[1], False, self.ws)
+
+        def norm(self):
+            c.coli_moe_block_norm_backward(T, H, do, None, s, y, pw, None, c.COLI_GATE_NONE, 0.5, qw,
+                                           EPS, self.res[2], self.res[3], self.res[4], self.res[5],
+                                           None, self.nws)
+
+        def wipe(self):
+            for t in self.res:
+                t.fill_(float("nan"))
+
+    a, b = Set(), Set()
+    a.products(), a.norm()
+    assert (a.ws[c.COLI_WS_HEADER_BYTES:] != 255).any()
+    want = [t.clone() for t in a.res]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(6):
+        a.wipe(), b.wipe()
+        torch.cuda.synchronize()
+        for st, v in zip(streams, (a, b)):
+            with torch.cuda.stream(st):
+                v.products(), v.norm(), v.products()
+        torch.cuda.synchronize()
+        for v in (a, b):
+            assert all(torch.equal(t, u) for t, u in zip(v.res, want))
+    graphs = []
+    for f in (lambda: (a.products(), a.norm()), lambda: (a.norm(), a.products())):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f()
+    for i in (0, 1, 1, 0, 0, 1):
+        a.wipe()
+        graphs[i].replay()
+        assert all(torch.equal(t, u) for t, u in zip(a.res, want))
+    for v in (a, b):
+        assert c.coli_moe_get_status(v.ws) == c.COLI_OK

@@ -337,3 +337,153 @@ def test_groups_inside_an_earlier_one_are_skipped(offsets, kept):
     assert torch.all(out[free] == 7) and torch.all(dx[free] == 7) and torch.all(o8[free] == 7)
     skipped = [e for e in range(E) if e not in [k[0] for k in kept]]
     assert torch.all(dw[skipped] == 7)
+
+
+def _poisoned(c, R, E):
+    """A workspace whose partial sums are NaN until a call writes them."""
+    ws = c.grouped_workspace(R, E)
+    ws[c.COLI_WS_HEADER_BYTES:].fill_(255)
+    return ws
+
+
+def _has_parts(c, ws):
+    return bool((ws[c.COLI_WS_HEADER_BYTES:] != 255).any())
+
+
+# tiles cut between workers (asserted: partial sums in the workspace), in every
+# direction: narrow tiles and pairs, several groups in one wave, ranges that start
+# and end inside a group or hold several groups, sizes that are no multiple of the
+# K-block or the MMA step
+CUT = [
+    ("mm", [1] * 8, 512, 6144),
+    ("mm", [3, 0, 40, 1], 264, 8200),
+    ("mm", [513], 2312, 6144),
+    ("dx", [8], 4096, 6144),
+    ("dx", [3, 0, 2, 3], 4104, 520),
+    ("dx", [513], 6144, 2312),
+    ("dw", [16371], 512, 512),
+    ("dw", [0, 9003, 0, 37, 7000, 0], 512, 520),
+    ("dw", [5000, 5001, 4999], 136, 264),
+]
+
+
+@pytest.mark.parametrize("out_dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("op,counts,N,K", CUT)
+def test_cut_tiles(op, counts, N, K, out_dt):
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    E = len(counts)
+    first, behind = 3, 5
+    off, o = _offsets(counts, first)
+    R = o[-1] + behind
+    g = _gen(N * 41 + K)
+    x, dy = _rn(g, R, K), _rn(g, R, N)
+    w = _rn(g, E, N, K, scale=0.1) if op != "dw" else None
+    for t in (x, dy):
+        t[:first] = NAN
+        t[o[-1]:] = float("inf")
+    shape = {"mm": (R, N), "dx": (R, K), "dw": (E, N, K)}[op]
+    outs = []
+    for _ in range(4):
+        out, ws = torch.full(shape, NAN, dtype=out_dt, device="cuda"), _poisoned(c, R, E)
+        if op == "mm":
+            c.coli_moe_grouped_mm(R, E, N, K, x, w, off, out, ws)
+        elif op == "dx":
+            c.coli_moe_grouped_mm_dx(R, E, N, K, dy, w, off, out, ws)
+        else:
+            c.coli_moe_grouped_mm_dw(R, E, N, K, dy, x, off, out, False, ws)
+        assert c.coli_moe_get_status(ws) == c.COLI_OK and _has_parts(c, ws)
+        outs.append(out)
+    for t in outs[1:]:       # added in a fixed order, whoever finishes last
+        assert torch.equal(t.view(torch.uint8), outs[0].view(torch.uint8))
+    for e in range(E):
+        lo, hi = o[e], o[e + 1]
+        X, D = x[lo:hi].double(), dy[lo:hi].double()
+        if op == "dw":
+            _check(outs[0][e], D.T @ X, D.abs().T @ X.abs(), hi - lo)
+            continue
+        W = w[e].double()
+        if op == "mm":
+            _check(outs[0][lo:hi], X @ W.T, X.abs() @ W.abs().T, K)
+        else:
+            _check(outs[0][lo:hi], D @ W, D.abs() @ W.abs(), N)
+    if op != "dw":
+        assert torch.isnan(outs[0][:first]).all() and torch.isnan(outs[0][o[-1]:]).all()
+
+
+@pytest.mark.parametrize("out_dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts,N,K", [([1] * 8, 512, 6144), ([513], 2312, 6144)])
+def test_fp8_cut_tiles(counts, N, K, out_dt):
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    E = len(counts)
+    off, o = _offsets(counts)
+    R, nb, kb = o[-1], -(-N // 128), -(-K // 128)
+    g = _gen(N * 43 + K)
+    x = _rn(g, R, K)
+    wq = _rn(g, E, N, K, dt=torch.float32, scale=100.0).clamp(-448, 448).to(torch.float8_e4m3fn)
+    sw = torch.rand(E, nb, kb, generator=g, device="cuda") * 1e-3 + 1e-4
+    xq = torch.empty(R, K, dtype=torch.float8_e4m3fn, device="cuda")
+    sx = torch.empty(kb, R, device="cuda")
+    c.coli_moe_fp8_quantize_rows(R, K, x, xq, sx)
+    outs = []
+    for _ in range(4):
+        out, ws = torch.full((R, N), NAN, dtype=out_dt, device="cuda"), _poisoned(c, R, E)
+        c.coli_moe_fp8_grouped_mm(R, E, N, K, xq, sx, wq, sw, off, out, ws)
+        assert c.coli_moe_get_status(ws) == c.COLI_OK and _has_parts(c, ws)
+        outs.append(out)
+    for t in outs[1:]:
+        assert torch.equal(t, outs[0])
+    X = xq.double() * sx.T.double().repeat_interleave(128, 1)[:, :K]
+    for e in range(E):
+        lo, hi = o[e], o[e + 1]
+        W = wq[e].double() * sw[e].double().repeat_interleave(128, 0)[:N] \
+            .repeat_interleave(128, 1)[:, :K]
+        _check(outs[0][lo:hi], X[lo:hi] @ W.T, X[lo:hi].abs() @ W.abs().T, K)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts,N,K", [([16371], 512, 512), ([0, 9003, 0, 37, 7000], 264, 520)])
+def test_cut_weight_gradient_accumulates(counts, N, K, dt):
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    off, o = _offsets(counts)
+    R, E = o[-1], len(counts)
+    g = _gen(12)
+    x, dy, dw = _rn(g, R, K), _rn(g, R, N), _rn(g, E, N, K, dt=dt)
+    old, ws = dw.double(), _poisoned(c, R, E)
+    c.coli_moe_grouped_mm_dw(R, E, N, K, dy, x, off, dw, True, ws)
+    assert c.coli_moe_get_status(ws) == c.COLI_OK and _has_parts(c, ws)
+    for e in range(E):
+        if counts[e] == 0:
+            assert torch.equal(dw[e].double(), old[e])
+            continue
+        X, D = x[o[e]:o[e + 1]].double(), dy[o[e]:o[e + 1]].double()
+        _check(dw[e], old[e] + D.T @ X, old[e].abs() + D.abs().T @ X.abs(), counts[e])
+
+
+@pytest.mark.parametrize("op,counts,N,K", [("mm", [64], 136, 16384), ("mm", [600], 2312, 16384),
+                                           ("dx", [64], 16384, 136), ("dx", [600], 16384, 2312),
+                                           ("dw", [16384], 264, 520)])
+def test_long_sums_leave_the_tensor_cores_in_chains(op, counts, N, K):
+    """Sums of 16384 positive products.  A chain of at most 768 products is 48
+    truncating additions of 16, each at most 2^-23 of the chain's sum; the 22 chains
+    (and up to 16 ranges of a cut tile) are added in fp32, each at most 2^-24 of the
+    whole: (48 + 19) 2^-23.  One chain of 16384, 1024 truncations of about half a
+    step of a sum that grows from nothing, is about 2e-5 off: more than twice that."""
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    g = _gen(13)
+    R, E = counts[0], 1
+
+    def pos(*shape):
+        return (torch.rand(*shape, generator=g, device="cuda") + 0.5).bfloat16()
+    off, ws = _offsets(counts)[0], c.grouped_workspace(R, E)
+    x, dy, w = pos(R, K), pos(R, N), pos(E, N, K)
+    if op == "mm":
+        out, ref = torch.empty(R, N, device="cuda"), x.double() @ w[0].double().T
+        c.coli_moe_grouped_mm(R, E, N, K, x, w, off, out, ws)
+    elif op == "dx":
+        out, ref = torch.empty(R, K, device="cuda"), dy.double() @ w[0].double()
+        c.coli_moe_grouped_mm_dx(R, E, N, K, dy, w, off, out, ws)
+    else:
+        out, ref = torch.empty(E, N, K, device="cuda"), (dy.double().T @ x.double())[None]
+        c.coli_moe_grouped_mm_dw(R, E, N, K, dy, x, off, out, False, ws)
+    assert c.coli_moe_get_status(ws) == c.COLI_OK
+    assert float(((out.double() - ref).abs() / ref).max()) <= 67 * 2.0 ** -23
