@@ -173,7 +173,7 @@ struct Shared {
     uint64_t tail_full[kMaxStages], tail_ready[kMaxStages];
     uint64_t mma_done;                     // after a timeout: no MMA is under way
     uint32_t tmem;
-    uint32_t loaded;                       // kDw: K-blocks loaded so far
+    uint32_t loaded;                       // kDw: K-blocks loaded, at the ring's last turn
     int bad;                               // an offset pair is impossible
     int abort;
     int kb_max;                            // K-blocks of the longest tile
@@ -629,10 +629,10 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                                 tc::tma_2d<CTAS>(sb, bmap, k, p.row0 + b0, bar);
                         }
                         ++it;
-                        if (MODE == kDw) *const_cast<volatile uint32_t*>(&s.loaded) = it;
                         if (++stage == kStages) {
                             stage = 0;
                             free ^= 1;
+                            if (MODE == kDw) *const_cast<volatile uint32_t*>(&s.loaded) = it;
                         }
                     }
                     if (!ok) break;
@@ -685,22 +685,21 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                     const uint32_t id =
                         tc::idesc(kBM * CTAS, mma_n<C>(p.n), FP8 ? 0 : 1, C::kAMn, C::kBMn);
                     const int len = chain_len<C, FP8>(p.kb1 - p.kb0);
-                    bool ok = true;
-                    for (int c0 = p.kb0; c0 < p.kb1 && ok; c0 += len) {
+                    for (int c0 = p.kb0; c0 < p.kb1; c0 += len) {
                         const int c1 = min(c0 + len, p.kb1);
-                        ok = tc::wait(aempty0 + buf * 8, drained, a.wait_ns);
-                        for (int kb = c0; kb < c1 && ok; ++kb) {
+                        if (!tc::wait(aempty0 + buf * 8, drained, a.wait_ns)) goto gave_up;
+                        for (int kb = c0; kb < c1; ++kb) {
                             const uint32_t d =
                                 tmem + (buf * C::kBatch + (C::kBatch > 1 ? kb - c0 : 0)) * C::BN;
-                            ok = tc::wait(full0 + stage * 8, full, a.wait_ns);
+                            if (!tc::wait(full0 + stage * 8, full, a.wait_ns)) goto gave_up;
                             const uint64_t ad = ad0 + stage * (C::kStage / 16);
                             const uint64_t bd = bd0 + stage * (C::kStage / 16);
                             if (MODE == kDw && p.rows - kb * C::BK < C::BK) {
                                 // a group's cut last K-block: whole MMA steps behind its
                                 // end are left out, warp 2 clears the rest of the last
-                                ok = ok && tc::wait_cluster(ready0 + stage * 8,
-                                                            tails >> stage & 1, a.wait_ns);
-                                if (!ok) break;
+                                if (!tc::wait_cluster(ready0 + stage * 8, tails >> stage & 1,
+                                                      a.wait_ns))
+                                    goto gave_up;
                                 tails ^= 1u << stage;
                                 tc::fence_after();
                                 const int steps = (p.rows - kb * C::BK + 15) / 16;
@@ -708,7 +707,6 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                                     tc::mma<FP8, CTAS>(d, ad + k * kAStep, bd + k * kBStep, id,
                                                        kb > c0 || k > 0);
                             } else {
-                                if (!ok) break;
                                 tc::fence_after();
                                 tc::mma<FP8, CTAS>(d, ad, bd, id, !FP8 && kb > c0);
 #pragma unroll
@@ -721,7 +719,6 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                                 full ^= 1;
                             }
                         }
-                        if (!ok) break;  // (no stage or accumulator of a failed wait is passed on)
                         tc::commit<CTAS>(afull0 + buf * 8);
                         buf = buf + 1 == C::kBufs ? 0 : buf + 1;
                         drained ^= buf == 0;
@@ -730,10 +727,10 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
                             looked = true;
                         }
                     }
-                    if (!ok) {
-                        timeout();
-                        break;
-                    }
+                    continue;
+                gave_up:  // no stage or accumulator of a failed wait is passed on
+                    timeout();
+                    break;
                 }
                 // after a timeout nobody waits for the last MMAs: they end before
                 // tensor memory is freed
@@ -831,7 +828,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const MmArgs a) {
         const uint32_t acc_empty =
             CTAS == 2 ? tc::cluster_addr(&s.acc_empty[0], 0) : smem_addr(&s.acc_empty[0]);
         uint32_t ch = 0;
-        while (!warp_aborted() && walk.next(p)) {
+        // (whoever gave up ends this loop too: the next accumulator does not come)
+        while (walk.next(p)) {
             // the two warps of a lane quarter share the columns evenly
             // (kFwdRows: the columns of one weight scale each)
             const int hn = C::kRows ? 128 : (p.n + 63) / 64 * 32;
