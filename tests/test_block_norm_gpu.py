@@ -350,3 +350,27 @@ def test_one_workspace_from_wide_to_narrow_rows():
         for k in got:
             tol = U * ref[k].abs() + (256 + T + 16) * U * mag[k]
             assert torch.all((got[k].double() - ref[k]).abs() <= tol), (H, k)
+
+
+@pytest.mark.parametrize("T,H,dt", [(700, 2048, torch.bfloat16), (600, 6144, torch.float32),
+                                    (40, 2048, torch.bfloat16), (300, 3001, torch.float32)])
+def test_in_place_gives_the_same_bits(T, H, dt):
+    """s over x and o over y; backward, dx over d_s and dy over d_o (all of one
+    type), in the kernels of many and of few rows."""
+    from int4_routed_expert_coli_b200 import coli_moe as c
+    v = _inputs(T, H, dt, dt, True, "channel", seed=T + H)
+    v["do"] = v["do"].to(dt)
+    s, o = torch.empty_like(v["x"]), torch.empty_like(v["y"])
+    args = (v["post_w"], v["gate"], c.COLI_GATE_CHANNEL, v["alpha"], v["pre_w"], EPS)
+    c.coli_moe_block_norm(T, H, v["x"], v["y"], *args, s, o)
+    x, y = v["x"].clone(), v["y"].clone()
+    c.coli_moe_block_norm(T, H, x, y, *args, x, y)
+    assert torch.equal(x, s) and torch.equal(y, o)
+    want = _backward(c, v, T, H, "channel")
+    ws = torch.empty(c.coli_moe_block_norm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
+    col = [torch.empty_like(want[k]) for k in ("dpre_w", "dpost_w", "dgate")]
+    do, ds = v["do"].clone(), v["ds"].clone()
+    c.coli_moe_block_norm_backward(T, H, do, ds, v["x"], v["y"], *args, ds, do, *col, ws)
+    assert torch.equal(ds, want["dx"]) and torch.equal(do, want["dy"])
+    for t, k in zip(col, ("dpre_w", "dpost_w", "dgate")):
+        assert torch.equal(t, want[k]), k
