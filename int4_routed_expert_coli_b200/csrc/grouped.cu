@@ -31,15 +31,20 @@
 // weights' stream bounds the call or few tiles would leave SMs idle (`narrow`).
 //
 // What bounds them, and the measured times (B200, one call between L2 flushes):
-//   * 8192 x 6144 x 6144 bf16 400 us, 1.54 PFLOP/s: the tensor cores at the clock
-//     the power limit leaves; e4m3 373 us: the drain, whose round trip (commit,
-//     wait, read, release) a K-block of 128 pays for, 0.76 us each, twice its MMAs;
-//   * 4096 rows of 32 experts of 4096 x 6144 bf16 301 us (weights alone 245 at a
-//     copy's rate), 8192 rows back to their gradient 376;
-//   * weight gradients of 16384 rows of the same experts 1050 us in fp32 (3.2 GB
-//     written: 490 at a copy's rate), 870 in bf16: loads and stores without MMAs
-//     take 1010, the stores' and loads' turns on the memory's bus;
-//   * one token's eight experts: bf16 69 us (5.85 TB/s), e4m3 42 (4.8 TB/s): the
+//   * 8192 x 6144 x 6144 bf16 405 us, 1.53 PFLOP/s (a stream of calls, at the 1.3
+//     GHz that the power limit leaves, 487): the tensor cores; e4m3 391 us: the
+//     drain, whose round trip (commit, wait, read, release) a K-block of 128 pays
+//     for, 0.76 us each, twice its MMAs;
+//   * 4096 rows of 32 experts of 4096 x 6144 bf16 308 us (weights alone 245 at a
+//     copy's rate), 8192 rows back to their gradient 365 (ten groups of more than
+//     256 rows read their weights twice);
+//   * weight gradients of 16384 rows of the same experts 1070 us in fp32 (3.2 GB
+//     written: 490 at a copy's rate), 900 in bf16.  In 1, 8, 32, 64 equal groups,
+//     with pauses, fp32 590, 625, 910, 1390 us, bf16 580, 580, 740, 1090: from 8 to
+//     64 the added results take their own time, 7.4 and 5.5 TB/s of them, as if
+//     nothing of it passed under the MMAs.  Added to what dw holds (32 groups):
+//     fp32 1510; bf16, each thread at its own row, 16 bytes at a time, 2170;
+//   * one token's eight experts: bf16 67 us (6.0 TB/s), e4m3 41 (4.9 TB/s): the
 //     weights' stream, and its start and end.
 //
 // Tiles: whole waves of tiles are dealt to the workers in order; the tiles of the
@@ -1217,7 +1222,9 @@ coli_status launch_mm(const void* A, const void* B, MmArgs a, int N, int K, cuda
 // And where they make a wave at most: wide ones would leave SMs without work (1024
 // x 1024 x 1024 narrow 9.7 us, wide 14.7; 2217 rows of 5 groups, N 472, K 1624 14.0
 // and 20.3, with more than a wave, for their 1624 columns, 18.1 and 14.5; 2048 x
-// 1024 x 2048, 1.7 waves, 23.7 and 20.1).
+// 1024 x 2048, 1.7 waves, 23.7 and 20.1).  The host does not know the groups' sizes and
+// goes by their average: where one of 128 groups holds all of 4096 rows, the call
+// takes 410 us, with wide tiles 157.
 bool narrow(int R, int E, int M) {
     const int64_t rows = (int64_t)R + 32 * (int64_t)E;  // half a tile lost per group
     return (int64_t)R <= 48 * (int64_t)E + 16 || rows * ((M + kBM - 1) / kBM) <= 64 * 160;

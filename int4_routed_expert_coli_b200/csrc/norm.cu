@@ -22,7 +22,10 @@
 // Both directions move each value once: 8 and 12 bytes a bf16 value.  4096 x 6144
 // bf16 with both norms and a channel gate takes 37.5 us forward (5.4 TB/s, 82 % of a
 // copy's rate) and 66 us backward (4.6 TB/s; a row's chain of loads, sums and stores
-// in few warps is what is left); 64 tokens 3.1 and 9.8 us, which is launches.
+// in few warps is what is left); 64 tokens 3.1 and 9.8 us, which is launches.  Rows
+// that are no whole vectors of 8, or wider than 8192, are read one by one with
+// nothing ahead of the one that reduces: 6140 wide 48 and 117 us, 6141 84 and 185,
+// 8200 75 and 265 (8192: 49 and 88).
 #include <algorithm>
 
 #include "coli_internal.cuh"
@@ -1010,7 +1013,9 @@ cudaError_t dispatch_ring(bool backward, const NormArgs& a, const RingPlan& p, i
 // Wider rows take more values a thread, up to what the registers hold (fp32, 4096
 // rows, forward and backward: 2001 values by 8 a thread 24.8 and 59.5 us, by 4 28.5
 // and 83.9; 1001 by 8 13.9 and 49.8, by 4 14.8 and 41.1; 2004 in 4 vectors a thread
-// 21.1 and 43.9, in 2 19.9 and 60.4).
+// 21.1 and 43.9, in 2 19.9 and 60.4).  With 32 values a thread, backward, six arrays
+// of them do not fit 128 registers: about 1 KB a thread spills (4096 x 16384 bf16
+// forward 158 us, backward 427).
 template <template <int, int> class Launch>
 cudaError_t dispatch_width(int H, int max_threads, const NormArgs& a, int grid, cudaStream_t st) {
     auto threads = [&](int vec, int nch) { return ((H + vec * nch - 1) / (vec * nch) + 31) / 32 * 32; };
