@@ -348,7 +348,8 @@ coli_status coli_moe_block_norm_backward(
  *       workspace of that size.  Device-side errors in its status word:
  *       BAD_INDEX (offsets that descend or leave [0, R]: those groups are
  *       skipped, and behind a descent those that start inside an earlier one:
- *       their rows, or dw, are left as they were), TIMEOUT.
+ *       their rows, or dw, are left as they were), TIMEOUT (the output is
+ *       undefined; clear the workspace before its next use).
  * Errors: INVALID_ARG (NULL, negative sizes, bad enum), SHAPE (E > 1024,
  * R > 2^24, N or K), ALIGN, WORKSPACE. */
 size_t coli_moe_grouped_workspace_size(int32_t R, int32_t E);
